@@ -110,6 +110,23 @@ typedef struct {
   int64_t dbias_slots; /* partial dBias tables in the workspace */
 } swin_attn_plan_info;
 
+/* Dropout decisions: Philox4x32-7 with key = seed and counter = (block low 32,
+ * block high 32, site, step). Decision i is 16-bit number i % 8 of block
+ * i / 8 (word (i % 8) / 2, low half first); it keeps iff that number is
+ * >= T = rint(rate * 65536), and what is kept is multiplied by
+ * 1 / (1 - T / 65536). What is dropped is 0 whatever it was (infinities and
+ * NaN too). The backward passes recompute the decisions: give them the same
+ * descriptor and an unchanged state. The state is read on the device when the
+ * kernel runs, so a captured call replays with the state's current step. Sites
+ * separate the dropouts of one step: two calls with one site, seed and step
+ * drop the same positions. */
+typedef struct {
+  double rate;           /* 0 (none) <= rate, T <= 65535 */
+  uint32_t site;
+  const uint64_t *state; /* device, 8-byte aligned: {seed, step}; the step counts modulo 2^32.
+                            May be NULL when the rate is 0 */
+} swin_attn_drop;
+
 /* Validate `desc` and build a plan on the current CUDA device: routing tables
  * (win_src, region, tok_dst, relidx) are computed on the device by the same
  * routing function the kernels use, and the work partition is fixed.
@@ -178,6 +195,27 @@ int swin_attn_bwd_o(swin_attn_plan_t plan, const void *q, const void *k, const v
                     void *dk, void *dv, float *dbias, void *workspace, size_t workspace_bytes,
                     swin_stream_t stream);
 
+/* swin_attn_fwd with dropout of the probabilities (drop NULL or rate 0: none):
+ *   O_i = sum over visible j of keep_ij / kept * softmax_ij * V_j;
+ * the log-sum-exp is the softmax's, without dropout. Decision of query token
+ * t (of image b, head h) and key slot j of its window of n slots:
+ * 8 * (r * ceil(n / 8)) + j with r = (b * heads + h) * tokens + t.
+ * head_dim 16 and 32 (head_dim 128 with a rate: UNSUPPORTED).
+ * Errors: those of swin_attn_fwd. */
+int swin_attn_fwd_dropout(swin_attn_plan_t plan, const void *q, const void *k, const void *v, const float *bias,
+                          const uint8_t *land, void *o, float *lse, const swin_attn_drop *drop,
+                          swin_stream_t stream);
+
+/* Its backward: with the same drop (and unchanged state) as the forward.
+ *   dP_ij = keep_ij / kept * (dO_i . V_j), dS_ij = P_ij (dP_ij - sum_j P_ij dP_ij),
+ *   dV_j = sum_i keep_ij / kept * P_ij dO_i.
+ * o, the forward's output, may be NULL. Other arguments, results and errors as
+ * swin_attn_bwd. */
+int swin_attn_bwd_dropout(swin_attn_plan_t plan, const void *q, const void *k, const void *v, const void *o,
+                          const void *dout, const float *lse, const float *bias, const uint8_t *land, void *dq,
+                          void *dk, void *dv, float *dbias, void *workspace, size_t workspace_bytes,
+                          const swin_attn_drop *drop, swin_stream_t stream);
+
 /* Backward for callers that cannot allocate device memory. No counterpart on
  * the pages: it exists for callers whose host code has no device allocator
  * of its own (for example a C or Fortran model that only receives tensors),
@@ -229,6 +267,92 @@ int swin_attn_block_fwd(swin_attn_plan_t plan, const void *x, const float *ln_ga
                         float ln_eps, const void *w_qkv, const float *b_qkv, const void *w_o,
                         const float *b_o, const float *bias, const uint8_t *land, void *y,
                         swin_stream_t stream);
+
+/* ---- Around the attention: norms, residual join, dropout -------------------
+ * These work on rows of `channels` values, one row per token of
+ * [images, tokens, channels] (the [B, grid..., C] tensors above with the grid
+ * flattened); no plan is needed. They run on the current device, to which
+ * every pointer must belong, allocate nothing and are asynchronous on
+ * `stream`. Activations are 16-byte, float parameters 4-byte, workspaces
+ * 256-byte aligned (ALIGNMENT). An output may be exactly one of the call's
+ * inputs of its own size (in place); outputs that overlap each other, or
+ * partly an input, are INVALID_ARG. With no rows nothing is read or written
+ * but the parameter gradients, which are zero. All sums are fp32 in a fixed
+ * order: the same inputs give the same bits. */
+
+#define SWIN_NORM_NONE 0
+#define SWIN_NORM_LAYER 1 /* (x - mean) / sqrt(var + eps), biased variance */
+#define SWIN_NORM_RMS 2   /* x / sqrt(mean of squares + eps) */
+typedef struct {
+  int32_t kind;       /* SWIN_NORM_* */
+  float eps;          /* > 0, finite */
+  const float *gamma; /* [C]; NULL: ones */
+  const float *beta;  /* [C]; NULL: zeros */
+} swin_attn_norm;
+
+typedef struct {
+  int64_t images, tokens; /* >= 0; images * tokens < 2^31 */
+  int32_t channels;       /* a multiple of 8, up to 8192 (else UNSUPPORTED) */
+  int32_t dtype;          /* SWIN_F32 or SWIN_BF16: the activations' type */
+} swin_attn_rows;
+
+/* Bytes of device workspace the backward calls on these rows need for any
+ * parameter gradient (0 for a bad descriptor). */
+size_t swin_attn_rows_workspace_bytes(const swin_attn_rows *rows);
+
+/* The norm before a block: h = N(x). norm->kind is not NONE.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA. */
+int swin_attn_norm_fwd(const swin_attn_rows *rows, const void *x, const swin_attn_norm *norm, void *h,
+                       swin_stream_t stream);
+
+/* Its backward: dx = dres + N^T dh (dres, the residual path's gradient, may be
+ * NULL), and, where not NULL, dgamma = sum dh xhat and dbeta = sum dh [C]
+ * (overwritten). The statistics are recomputed from x. The workspace is
+ * needed for dgamma or dbeta only (WORKSPACE).
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+int swin_attn_norm_bwd(const swin_attn_rows *rows, const void *x, const swin_attn_norm *norm, const void *dh,
+                       const void *dres, void *dx, float *dgamma, float *dbeta, void *workspace,
+                       size_t workspace_bytes, swin_stream_t stream);
+
+/* The residual join after a block whose output is z, with the next block's
+ * norm:
+ *   y = x + scale * gate * path * D(N_post(z)),   h = N_pre(y),
+ * y rounded to the activations' type and h the norm of that stored y.
+ * N_post and N_pre may be NONE (pre NONE: h is NULL). D: dropout of the
+ * elements, element e of [images, tokens, C] being decision e. path: dropout
+ * of whole images (stochastic depth), image b being decision b. */
+typedef struct {
+  swin_attn_norm post, pre;
+  const float *scale; /* [C] layer scale; NULL: ones */
+  const float *gate;  /* [images][C]; NULL: ones */
+  swin_attn_drop drop, path;
+} swin_attn_join;
+
+/* Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA. */
+int swin_attn_join_fwd(const swin_attn_rows *rows, const void *x, const void *z, const swin_attn_join *join,
+                       void *y, void *h, swin_stream_t stream);
+
+/* Gradients of the join's parameters, each NULL where not wanted; gate is
+ * [images][C], the others [C]. All are overwritten. */
+typedef struct {
+  float *post_gamma, *post_beta, *scale, *gate, *pre_gamma, *pre_beta;
+} swin_attn_join_grads;
+
+/* Backward of the join from its stored y (not x) and z: dx and dz. dy or dh
+ * may be NULL (zero gradient), not both; y may be NULL when dh is, z when
+ * there is no post norm and neither scale's nor gate's gradient is wanted.
+ * The workspace is needed for parameter gradients only.
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+int swin_attn_join_bwd(const swin_attn_rows *rows, const void *y, const void *z, const swin_attn_join *join,
+                       const void *dy, const void *dh, void *dx, void *dz, const swin_attn_join_grads *grads,
+                       void *workspace, size_t workspace_bytes, swin_stream_t stream);
+
+/* Dropout of n elements of type dtype: y_i = keep(i / span) ? x_i / kept : 0,
+ * `span` consecutive elements sharing one decision (1: dropout; tokens * C:
+ * stochastic depth per image). Its backward is the same call on the gradient.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA. */
+int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, const swin_attn_drop *drop, void *y,
+                      swin_stream_t stream);
 
 /* Testing hook for the failure path of the tensor-core kernels (the fused
  * block's included). Every wait inside those kernels gives up after

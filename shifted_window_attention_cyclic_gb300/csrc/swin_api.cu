@@ -67,7 +67,7 @@ __global__ void fold_kernel(FoldArgs a) {
   const int t = x / a.heads, h = x % a.heads;
   float sum = 0.f;
   for (int s = a.head_slot_begin[h]; s < a.head_slot_begin[h + 1]; ++s) sum += a.ws[(int64_t)s * a.T + t];
-  a.dbias[x] = sum;
+  a.dbias[x] = sum * a.scale;
 }
 
 constexpr int64_t kMaxSlots = 65536;       // slots per window
@@ -355,8 +355,12 @@ size_t swin_attn_workspace_bytes(swin_attn_plan_t p) {
   return delta_bytes(p) + ((bytes + 255) & ~size_t(255));
 }
 
-int swin_attn_fwd(swin_attn_plan_t p, const void *q, const void *k, const void *v, const float *bias,
-                  const uint8_t *land, void *o, float *lse, swin_stream_t stream) {
+}  // extern "C"
+
+namespace {
+// swin_attn_fwd and swin_attn_fwd_dropout: drop may be NULL.
+int fwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, const float *bias, const uint8_t *land,
+             void *o, float *lse, const swin_attn_drop *drop, swin_stream_t stream) {
   if (!p || !q || !k || !v || !o) return SWIN_ERR_INVALID_ARG;
   if (p->d.has_land && !land) return SWIN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return SWIN_ERR_ALIGNMENT;
@@ -364,9 +368,12 @@ int swin_attn_fwd(swin_attn_plan_t p, const void *q, const void *k, const void *
   // consecutive tokens: 16 and 4 bytes
   if ((bias && !aligned4(bias)) || (lse && !aligned16(lse)) || (p->d.has_land && !aligned4(land)))
     return SWIN_ERR_ALIGNMENT;
-  int rc = current_device_matches(p);
-  if (rc) return rc;
   FwdArgs a;
+  int rc = make_drop(drop, &a.drop);
+  if (rc) return rc;
+  if (a.drop.thr && p->large) return SWIN_ERR_UNSUPPORTED;  // the key-tiled kernels have no dropout
+  rc = current_device_matches(p);
+  if (rc) return rc;
   a.g = p->g;
   a.q = q;
   a.k = k;
@@ -386,13 +393,10 @@ int swin_attn_fwd(swin_attn_plan_t p, const void *q, const void *k, const void *
   return launch_fwd_simt(a, p->d.dtype, stream);
 }
 
-}  // extern "C"
-
-namespace {
-// swin_attn_bwd and swin_attn_bwd_o: o (the forward's output) may be NULL.
+// swin_attn_bwd, swin_attn_bwd_o and swin_attn_bwd_dropout: o (the forward's output) and drop may be NULL.
 int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, const void *o, const void *dout,
              const float *lse, const float *bias, const uint8_t *land, void *dq, void *dk, void *dv, float *dbias,
-             void *workspace, size_t workspace_bytes, swin_stream_t stream) {
+             void *workspace, size_t workspace_bytes, const swin_attn_drop *drop, swin_stream_t stream) {
   if (!p || !q || !k || !v || !dout || !lse || !dq || !dk || !dv) return SWIN_ERR_INVALID_ARG;
   if (o && !aligned16(o)) return SWIN_ERR_ALIGNMENT;
   if (p->d.has_land && !land) return SWIN_ERR_INVALID_ARG;
@@ -406,9 +410,12 @@ int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
     if (!workspace || workspace_bytes < swin_attn_workspace_bytes(p)) return SWIN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return SWIN_ERR_ALIGNMENT;
   }
-  int rc = current_device_matches(p);
-  if (rc) return rc;
   BwdArgs a;
+  int rc = make_drop(drop, &a.drop);
+  if (rc) return rc;
+  if (a.drop.thr && p->large) return SWIN_ERR_UNSUPPORTED;  // the key-tiled kernels have no dropout
+  rc = current_device_matches(p);
+  if (rc) return rc;
   a.g = p->g;
   a.q = q;
   a.k = k;
@@ -440,6 +447,7 @@ int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
   f.dbias = dbias;
   f.T = p->g.T;
   f.heads = p->g.heads;
+  f.scale = a.drop.scale;  // the kernels leave the kept values' scale out of dS
   const int total = f.T * f.heads;
   fold_kernel<<<(total + 255) / 256, 256, 0, static_cast<cudaStream_t>(stream)>>>(f);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
@@ -448,18 +456,37 @@ int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
 
 extern "C" {
 
+int swin_attn_fwd(swin_attn_plan_t p, const void *q, const void *k, const void *v, const float *bias,
+                  const uint8_t *land, void *o, float *lse, swin_stream_t stream) {
+  return fwd_impl(p, q, k, v, bias, land, o, lse, nullptr, stream);
+}
+
+int swin_attn_fwd_dropout(swin_attn_plan_t p, const void *q, const void *k, const void *v, const float *bias,
+                          const uint8_t *land, void *o, float *lse, const swin_attn_drop *drop,
+                          swin_stream_t stream) {
+  return fwd_impl(p, q, k, v, bias, land, o, lse, drop, stream);
+}
+
 int swin_attn_bwd(swin_attn_plan_t p, const void *q, const void *k, const void *v, const void *dout,
                   const float *lse, const float *bias, const uint8_t *land, void *dq, void *dk, void *dv,
                   float *dbias, void *workspace, size_t workspace_bytes, swin_stream_t stream) {
   return bwd_impl(p, q, k, v, nullptr, dout, lse, bias, land, dq, dk, dv, dbias, workspace, workspace_bytes,
-                  stream);
+                  nullptr, stream);
 }
 
 int swin_attn_bwd_o(swin_attn_plan_t p, const void *q, const void *k, const void *v, const void *o,
                     const void *dout, const float *lse, const float *bias, const uint8_t *land, void *dq, void *dk,
                     void *dv, float *dbias, void *workspace, size_t workspace_bytes, swin_stream_t stream) {
   if (!o) return SWIN_ERR_INVALID_ARG;
-  return bwd_impl(p, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace, workspace_bytes, stream);
+  return bwd_impl(p, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace, workspace_bytes, nullptr,
+                  stream);
+}
+
+int swin_attn_bwd_dropout(swin_attn_plan_t p, const void *q, const void *k, const void *v, const void *o,
+                          const void *dout, const float *lse, const float *bias, const uint8_t *land, void *dq,
+                          void *dk, void *dv, float *dbias, void *workspace, size_t workspace_bytes,
+                          const swin_attn_drop *drop, swin_stream_t stream) {
+  return bwd_impl(p, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace, workspace_bytes, drop, stream);
 }
 
 int swin_attn_block_fwd(swin_attn_plan_t p, const void *x, const float *ln_gamma, const float *ln_beta,

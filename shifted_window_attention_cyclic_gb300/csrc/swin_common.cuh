@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "../../include/swin_attn.h"
+#include "swin_philox.cuh"
 
 namespace swin {
 
@@ -220,6 +221,7 @@ struct FwdArgs {
   float scale;  // hd^-1/2
   uint64_t wait_limit_ns;   // bound of every in-kernel wait
   int debug_force_timeout;  // testing hook: one role waits on a barrier nothing arrives at
+  Drop drop;                // dropout of the probabilities (thr 0: none)
 };
 
 struct BwdArgs {
@@ -239,6 +241,7 @@ struct BwdArgs {
   float scale;
   uint64_t wait_limit_ns;
   int debug_force_timeout;
+  Drop drop;
 };
 
 struct FoldArgs {
@@ -246,6 +249,7 @@ struct FoldArgs {
   const int *head_slot_begin;  // [heads + 1] slot range of every head
   float *dbias;                // [T][heads]
   int T, heads;
+  float scale;                 // of the sums: 1, or the kept values' dropout scale
 };
 
 // The attention half of a Swin block (swin_block.cu): LayerNorm + QKV

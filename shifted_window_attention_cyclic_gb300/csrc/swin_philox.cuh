@@ -1,0 +1,100 @@
+// swin_philox.cuh -- dropout decisions from a counter-based generator.
+//
+// Philox4x32-7 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy
+// as 1, 2, 3", SC 2011; seven rounds are the fewest the paper reports to pass
+// every BigCrush test): the 64-bit seed is the key, the counter is (block low,
+// block high, site, step). One block's 128 bits are eight 16-bit numbers, so
+// eight decisions: decision i is number i % 8 of block i / 8 (word (i % 8) / 2,
+// low half first) and keeps iff the number is >= T = rint(rate * 65536). A
+// decision is a pure function of (seed, step, site, i): forward and backward
+// recompute it, whatever tiles their kernels use, and no mask is stored.
+// 16 bits per decision, not 32: half the generator's work, and rates are
+// honoured to 2^-17; the kept values' scale is 1 / (1 - T / 65536), the exact
+// inverse of the share that is kept.
+#pragma once
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/swin_attn.h"
+
+namespace swin {
+
+// A dropout as the kernels take it; thr == 0 means none.
+struct Drop {
+  uint32_t thr;           // T
+  uint32_t site;
+  float scale;            // 65536 / (65536 - T)
+  const uint64_t *state;  // device: {seed, step}
+};
+
+// Checks and converts the caller's descriptor (NULL or rate 0: no dropout).
+inline int make_drop(const swin_attn_drop *d, Drop *out) {
+  *out = Drop{0u, 0u, 1.f, nullptr};
+  if (!d) return SWIN_OK;
+  if (!(d->rate >= 0.0 && d->rate < 1.0)) return SWIN_ERR_INVALID_ARG;
+  const double t = std::rint(d->rate * 65536.0);
+  if (t == 0.0) return SWIN_OK;
+  if (t > 65535.0 || !d->state) return SWIN_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(d->state) & 7u) return SWIN_ERR_ALIGNMENT;
+  out->thr = (uint32_t)t;
+  out->site = d->site;
+  out->scale = (float)(65536.0 / (65536.0 - t));
+  out->state = d->state;
+  return SWIN_OK;
+}
+
+// The generator of one dropout in one launch.
+struct Philox {
+  uint32_t k0, k1, site, step;
+
+  __device__ __forceinline__ void init(const Drop &d) {
+    k0 = k1 = step = 0u;
+    site = d.site;
+    if (d.thr) {
+      const uint64_t seed = __ldg(reinterpret_cast<const unsigned long long *>(d.state));
+      k0 = (uint32_t)seed;
+      k1 = (uint32_t)(seed >> 32);
+      step = (uint32_t)__ldg(reinterpret_cast<const unsigned long long *>(d.state) + 1);
+    }
+  }
+
+  // The eight 16-bit numbers of a block, two per word, low half first.
+  __device__ __forceinline__ uint4 block(uint64_t b) const {
+    uint32_t c0 = (uint32_t)b, c1 = (uint32_t)(b >> 32), c2 = site, c3 = step, a = k0, k = k1;
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+      const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+      c0 = (uint32_t)(p1 >> 32) ^ c1 ^ a;
+      c1 = (uint32_t)p1;
+      c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k;
+      c3 = (uint32_t)p0;
+      a += 0x9E3779B9u;
+      k += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+  }
+};
+
+// Decision e (a compile-time 0..7 after unrolling) of a block.
+__device__ __forceinline__ bool keep_of(const uint4 &u, int e, uint32_t thr) {
+  const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
+  return ((e & 1) ? (w >> 16) : (w & 0xFFFFu)) >= thr;
+}
+
+// A block's eight decisions, bit e = decision e keeps.
+__device__ __forceinline__ uint32_t keep_bits(const uint4 &u, uint32_t thr) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m |= keep_of(u, e, thr) ? 1u << e : 0u;
+  return m;
+}
+
+// One decision, alone.
+__device__ __forceinline__ bool keep_one(const Philox &ph, uint64_t i, uint32_t thr) {
+  const uint4 u = ph.block(i >> 3);
+  const int e = (int)(i & 7);
+  const uint32_t w = (e >> 1) == 0 ? u.x : (e >> 1) == 1 ? u.y : (e >> 1) == 2 ? u.z : u.w;
+  return ((e & 1) ? (w >> 16) : (w & 0xFFFFu)) >= thr;
+}
+
+}  // namespace swin

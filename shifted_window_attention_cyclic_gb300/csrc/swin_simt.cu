@@ -109,7 +109,9 @@ __host__ __device__ inline int fwd_smem_bytes(int T) {
   return (2 * kThreads * HD + round4(T)) * 4 + 2 * kThreads * 4;
 }
 
-template <typename T, int HD>
+// kDrop: dropout of the probabilities; a thread draws its row's decisions one
+// block of eight keys at a time.
+template <typename T, int HD, bool kDrop>
 __global__ void __launch_bounds__(kThreads) fwd_simt_kernel(const FwdArgs a) {
   extern __shared__ float4 smem4[];
   float *sK = reinterpret_cast<float *>(smem4);
@@ -122,6 +124,9 @@ __global__ void __launch_bounds__(kThreads) fwd_simt_kernel(const FwdArgs a) {
   int64_t L, R;
   eq4_range(a.items, a.ctas, blockIdx.x, L, R);
   int cur_h = -1;
+  Philox ph;
+  if (kDrop) ph.init(a.drop);
+  const int nb = (g.n + 7) >> 3;  // blocks of a row's decisions
   for (int64_t it = L; it < R; ++it) {
     const Item x = decode_item(g, it);
     if (x.h != cur_h) {
@@ -156,7 +161,10 @@ __global__ void __launch_bounds__(kThreads) fwd_simt_kernel(const FwdArgs a) {
       for (int c = 0; c < HD; ++c) acc[c] = 0.f;
       float m = -INFINITY, l = 0.f, lse = -INFINITY, inv = 0.f;
       if (live) {
+        const uint64_t blk0 = (((uint64_t)x.b * g.heads + x.h) * g.tokens + r.src) * nb;
+        uint32_t keep = ~0u;
         for (int j = 0; j < g.n; ++j) {
+          if (kDrop && (j & 7) == 0) keep = keep_bits(ph.block(blk0 + (j >> 3)), a.drop.thr);
           if (sCode[j] != r.reg) continue;
           const float s = dot_row<HD>(q, sK + j * HD) * a.scale + sB[r.rbase - sRoff[j]];
           if (s > m) {
@@ -168,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) fwd_simt_kernel(const FwdArgs a) {
           }
           const float p = expf(s - m);
           l += p;
-          axpy_row<HD>(acc, p, sV + j * HD);
+          if (!kDrop || ((keep >> (j & 7)) & 1u)) axpy_row<HD>(acc, p, sV + j * HD);
         }
-        inv = 1.f / l;
+        inv = (kDrop ? a.drop.scale : 1.f) / l;
         lse = m + logf(l);
       }
       RowIO<T, HD>::store(static_cast<T *>(a.o) + tok * g.C + (int64_t)x.h * HD, acc, inv);
@@ -184,6 +192,8 @@ __global__ void __launch_bounds__(kThreads) fwd_simt_kernel(const FwdArgs a) {
 // smem: Q, K, V, dO tiles [128][HD]; lse, delta [128]; bias column [T];
 // key codes, query codes, key offsets, query bases [128]; partial dBias
 // [128][129] accumulated over the CTA's windows of one head.
+// With dropout, sKeep[query][4]: the decisions of the row's up to 128 keys, drawn
+// by the query's thread in pass A and read by the keys' threads in pass B.
 constexpr int kPartStride = kThreads + 1;
 
 template <int HD>
@@ -217,9 +227,10 @@ __device__ void flush_partial(const Geo &g, float *sPart, float *ws, int slot) {
   __syncthreads();
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool kDrop>
 __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
   extern __shared__ float4 smem4[];
+  __shared__ uint32_t sKeep[kDrop ? kThreads * 5 : 1];  // [query][4], padded to 5 words
   float *sQ = reinterpret_cast<float *>(smem4);
   float *sK = sQ + kThreads * HD;
   float *sV = sK + kThreads * HD;
@@ -240,6 +251,10 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
   if (L >= R) return;
   const int h_first = decode_item(g, L).h;
   int cur_h = -1;
+  Philox ph;
+  if (kDrop) ph.init(a.drop);
+  const int nb = (g.n + 7) >> 3;
+  auto kept = [&](int i, int j) { return !kDrop || ((sKeep[i * 5 + (j >> 5)] >> (j & 31)) & 1u); };
   for (int64_t it = L; it < R; ++it) {
     const Item x = decode_item(g, it);
     if (x.h != cur_h) {
@@ -282,20 +297,30 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
         dq[c] = 0.f;
       }
       const float lse = sLse[tid];
+      if (kDrop) {
+        const uint64_t blk0 = (((uint64_t)x.b * g.heads + x.h) * g.tokens + r.src) * nb;
+        for (int w = 0; w < (nb + 3) >> 2; ++w) {
+          uint32_t bits = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bits |= keep_bits(ph.block(blk0 + 4 * w + k), a.drop.thr) << (8 * k);
+          sKeep[tid * 5 + w] = bits;
+        }
+      }
       for (int j = 0; j < g.n; ++j) {
         if (sKcode[j] != r.reg) continue;
         const float s = dot_row<HD>(qi, sK + j * HD) * a.scale + sB[r.rbase - sRoff[j]];
-        delta = fmaf(expf(s - lse), dot_row<HD>(doi, sV + j * HD), delta);
+        // the kept values' scale is left out of dP and dS here; dq, dk, dv and dBias take it at the end
+        if (kept(tid, j)) delta = fmaf(expf(s - lse), dot_row<HD>(doi, sV + j * HD), delta);
       }
       for (int j = 0; j < g.n; ++j) {
         if (sKcode[j] != r.reg) continue;
         const float s = dot_row<HD>(qi, sK + j * HD) * a.scale + sB[r.rbase - sRoff[j]];
         const float p = expf(s - lse);
-        const float ds = p * (dot_row<HD>(doi, sV + j * HD) - delta);
+        const float ds = p * ((kept(tid, j) ? dot_row<HD>(doi, sV + j * HD) : 0.f) - delta);
         axpy_row<HD>(dq, ds, sK + j * HD);
         sPart[tid * kPartStride + j] += ds;
       }
-      RowIO<T, HD>::store(static_cast<T *>(a.dq) + tok * g.C + (int64_t)x.h * HD, dq, a.scale);
+      RowIO<T, HD>::store(static_cast<T *>(a.dq) + tok * g.C + (int64_t)x.h * HD, dq, kDrop ? a.scale * a.drop.scale : a.scale);
     } else if (r.src >= 0) {
       float z[HD];
 #pragma unroll
@@ -320,13 +345,14 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
           if (sQcode[i] != r.reg) continue;
           const float s = dot_row<HD>(kj, sQ + i * HD) * a.scale + sB[sRbase[i] - r.roff];
           const float p = expf(s - sLse[i]);
-          const float ds = p * (dot_row<HD>(vj, sdO + i * HD) - sDelta[i]);
+          const bool keep = kept(i, tid);
+          const float ds = p * ((keep ? dot_row<HD>(vj, sdO + i * HD) : 0.f) - sDelta[i]);
           axpy_row<HD>(dk, ds, sQ + i * HD);
-          axpy_row<HD>(dv, p, sdO + i * HD);
+          if (keep) axpy_row<HD>(dv, p, sdO + i * HD);
         }
       }
-      RowIO<T, HD>::store(static_cast<T *>(a.dk) + tok * g.C + (int64_t)x.h * HD, dk, a.scale);
-      RowIO<T, HD>::store(static_cast<T *>(a.dv) + tok * g.C + (int64_t)x.h * HD, dv, 1.f);
+      RowIO<T, HD>::store(static_cast<T *>(a.dk) + tok * g.C + (int64_t)x.h * HD, dk, kDrop ? a.scale * a.drop.scale : a.scale);
+      RowIO<T, HD>::store(static_cast<T *>(a.dv) + tok * g.C + (int64_t)x.h * HD, dv, kDrop ? a.drop.scale : 1.f);
     }
     __syncthreads();
   }
@@ -336,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
 template <typename T, int HD>
 int launch_fwd_t(const FwdArgs &a, cudaStream_t st) {
   const int smem = fwd_smem_bytes<HD>(a.g.T);
-  auto kern = fwd_simt_kernel<T, HD>;
+  auto kern = a.drop.thr ? fwd_simt_kernel<T, HD, true> : fwd_simt_kernel<T, HD, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, kThreads, smem, st>>>(a);
@@ -346,7 +372,7 @@ int launch_fwd_t(const FwdArgs &a, cudaStream_t st) {
 template <typename T, int HD>
 int launch_bwd_t(const BwdArgs &a, cudaStream_t st) {
   const int smem = bwd_smem_bytes<HD>(a.g.T);
-  auto kern = bwd_simt_kernel<T, HD>;
+  auto kern = a.drop.thr ? bwd_simt_kernel<T, HD, true> : bwd_simt_kernel<T, HD, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, kThreads, smem, st>>>(a);
@@ -377,11 +403,11 @@ int simt_occupancy(bool bwd, const Geo &g, int dtype, int *blocks_per_sm) {
   const int smem = bwd ? simt_bwd_smem(g) : simt_fwd_smem(g);
   const void *fn;
   if (g.hd == 16)
-    fn = bwd ? (dtype == SWIN_BF16 ? (const void *)bwd_simt_kernel<__nv_bfloat16, 16> : (const void *)bwd_simt_kernel<float, 16>)
-             : (dtype == SWIN_BF16 ? (const void *)fwd_simt_kernel<__nv_bfloat16, 16> : (const void *)fwd_simt_kernel<float, 16>);
+    fn = bwd ? (dtype == SWIN_BF16 ? (const void *)bwd_simt_kernel<__nv_bfloat16, 16, false> : (const void *)bwd_simt_kernel<float, 16, false>)
+             : (dtype == SWIN_BF16 ? (const void *)fwd_simt_kernel<__nv_bfloat16, 16, false> : (const void *)fwd_simt_kernel<float, 16, false>);
   else
-    fn = bwd ? (dtype == SWIN_BF16 ? (const void *)bwd_simt_kernel<__nv_bfloat16, 32> : (const void *)bwd_simt_kernel<float, 32>)
-             : (dtype == SWIN_BF16 ? (const void *)fwd_simt_kernel<__nv_bfloat16, 32> : (const void *)fwd_simt_kernel<float, 32>);
+    fn = bwd ? (dtype == SWIN_BF16 ? (const void *)bwd_simt_kernel<__nv_bfloat16, 32, false> : (const void *)bwd_simt_kernel<float, 32, false>)
+             : (dtype == SWIN_BF16 ? (const void *)fwd_simt_kernel<__nv_bfloat16, 32, false> : (const void *)fwd_simt_kernel<float, 32, false>);
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return SWIN_ERR_CUDA;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, fn, kThreads, smem);

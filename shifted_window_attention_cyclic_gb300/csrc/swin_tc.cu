@@ -531,7 +531,11 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 
 // kPack: windows per work item (1 or 2), a compile-time copy per value so
 // that the one-window kernel carries no code for the second window.
-template <int kPack>
+// kDrop: dropout of the probabilities. Thread (grp, i) draws the decisions of
+// its own row and keys beside the exponentials (one generator block per eight
+// keys), so no mask exists anywhere; the row sums are taken before it, and the
+// kept values' scale goes into the epilogue's 1 / l.
+template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_tc_kernel(const FwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
                   const __grid_constant__ TmaSet tmv) {
@@ -737,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m = two ? fmaxf(m0, m1) : m0;
         const float a0 = ex2(m0 - m), a1 = two ? ex2(m1 - m) : 0.f;
         const float l = two ? fmaf(a0, l0, a1 * l1) : l0;
-        const float inv = live ? __frcp_rn(l) : 0.f;
+        const float inv = live ? (kDrop ? a.drop.scale * __frcp_rn(l) : __frcp_rn(l)) : 0.f;
         const float c0 = a0 * inv, c1 = a1 * inv;
         uint32_t w[16];
 #pragma unroll
@@ -796,6 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h_last = count > 0 ? decode_item(g, R - 1).h : 0;  // heads rise by one along the range
     uint32_t bs_phase = 0;
     float *bvec = reinterpret_cast<float *>(smem + kBvec);
+    Philox ph;
+    if (kDrop) ph.init(a.drop);
+    const int nb = (g.n + 7) >> 3;                // generator blocks of a row's keys
+    const int kb0 = kPack == 2 ? 0 : 2 * gb;      // block of this thread's first key
     bool ok = true;
     if (a.debug_force_timeout && grp == 0) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     ItemCursor x;
@@ -843,6 +851,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_warp(bar(bPFull + wb));
         continue;
       }
+      uint64_t blk = 0;
+      if (kDrop) {  // the row's query token (the stage is held until this item's P is consumed)
+        if (!mbar_wait_warp(bar(bFull + (int)(it % kStages)), (uint32_t)(it / kStages) & 1u, ctl)) break;
+        const int src = reinterpret_cast<const int *>(smem + (int)(it % kStages) * kStageBytes + kMeta)[i];
+        blk = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + kb0;
+      }
       uint32_t sv[4][16];
 #pragma unroll
       for (int k4 = 0; k4 < 4; ++k4)
@@ -878,12 +892,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k4 = 0; k4 < 4; ++k4) {
         if (gb + k4 < ge) {
           uint32_t pv[8];
+          uint4 bits = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const float2 xs2 =
                 __fadd2_rn(make_float2(__uint_as_float(sv[k4][e]), __uint_as_float(sv[k4][e + 1])), negm);
-            const float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
+            float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
             sp2[(e >> 1) & 3] = __fadd2_rn(sp2[(e >> 1) & 3], p);
+            if (kDrop) {
+              if ((e & 7) == 0) bits = ph.block(blk + 2 * k4 + (e >> 3));
+              p.x = keep_of(bits, e & 7, a.drop.thr) ? p.x : 0.f;
+              p.y = keep_of(bits, (e & 7) + 1, a.drop.thr) ? p.y : 0.f;
+            }
             pv[e >> 1] = pack_bf16(p.x, p.y);
           }
           tmem_st8(tS + 16u * (gb + k4), pv);  // over the first half of its own S group
@@ -959,7 +979,12 @@ __device__ __forceinline__ uint32_t pds_chunk(int i, int c) {
   return (c >> 3) * 16384 + (i >> 3) * 1024 + (i & 7) * 128 + (((c & 7) ^ (i & 7)) << 4);
 }
 
-template <int kPack>
+// kDrop: pass 1 draws the forward's decisions again; a dropped key's dP is
+// zeroed where it lies in TMEM (pass 2 then needs no decisions) and its P in
+// the dV operand. The kept values' scale c is left out of both passes
+// (dS / c = P (keep dP - sum P keep dP)) and taken by the epilogue's multiplier
+// of dV, dK and dQ and by the dBias fold.
+template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_tc_kernel(const BwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
                   const __grid_constant__ TmaSet tmv, const __grid_constant__ TmaSet tmdo) {
@@ -1140,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = 0; t < 3; ++t) {
         drain(t == 0 ? (vb ? kColdV1 : kColdV) : t == 1 ? kColdK : kColdQ, t == 0 ? a.dv : t == 1 ? a.dk : a.dq,
-              t == 0 ? 1.f : a.scale);
+              (t == 0 ? 1.f : a.scale) * (kDrop ? a.drop.scale : 1.f));
         if (t == 0) {
           tc_fence_before();
           mbar_arrive_warp(bar(bVFree + vb));
@@ -1180,6 +1205,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cur_h = -1, h_first = -1;
     const int h_last = count > 0 ? decode_item(g, R - 1).h : 0;  // heads rise by one along the range
     uint32_t wsync_phase = 0;
+    Philox ph;
+    if (kDrop) ph.init(a.drop);
+    const int nb = (g.n + 7) >> 3;            // generator blocks of a row's keys
+    const int kg0 = kPack == 2 ? gb : 0;      // group that holds the row's window's first key
     bool ok = true;
     if (a.debug_force_timeout) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     // Fold the slot-pair dBias accumulator into bias rows (fixed order) and
@@ -1264,9 +1293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // pass 1: P = exp2(S*cs + bias2 - lse2); partial delta = sum_j P dP over
       // this half; P (fp32) back over S in TMEM, P (bf16) to the smem tile.
       float delta = 0.f;
+      uint64_t blk = 0;  // the row's first generator block
+      if (kDrop)
+        blk = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(reinterpret_cast<const int *>(sp + kMeta)[i], 0)) * nb;
       const float2 nl2 = make_float2(-lse2, -lse2);
       auto p_group = [&](int gi, uint32_t (&sv)[16], uint32_t (&dpv)[16]) {
         uint32_t pb[8];
+        uint4 bits = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int e4 = 0; e4 < 16; e4 += 4) {
           const float4 b4 = *reinterpret_cast<const float4 *>(brow + 16 * gi + e4);
@@ -1277,14 +1310,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    make_float2(bb[e - e4], bb[e - e4 + 1]));
             xs = __fadd2_rn(xs, nl2);
             const float p0 = live ? ex2(xs.x) : 0.f, p1 = live ? ex2(xs.y) : 0.f;
+            bool k0 = true, k1 = true;
+            if (kDrop) {
+              if ((e & 7) == 0) bits = ph.block(blk + 2 * (gi - kg0) + (e >> 3));
+              k0 = keep_of(bits, e & 7, a.drop.thr);
+              k1 = keep_of(bits, (e & 7) + 1, a.drop.thr);
+              dpv[e] = k0 ? dpv[e] : 0u;
+              dpv[e + 1] = k1 ? dpv[e + 1] : 0u;
+            }
             delta = fmaf(p0, __uint_as_float(dpv[e]), delta);
             delta = fmaf(p1, __uint_as_float(dpv[e + 1]), delta);
             sv[e] = __float_as_uint(p0);  // P (fp32) overwrites S in the register buffer
             sv[e + 1] = __float_as_uint(p1);
-            pb[e >> 1] = pack_bf16(p0, p1);
+            pb[e >> 1] = pack_bf16(k0 ? p0 : 0.f, k1 ? p1 : 0.f);
           }
         }
         tmem_st16(tS + 16u * gi, sv);
+        if (kDrop) tmem_st16(tdP + 16u * gi, dpv);
         *reinterpret_cast<uint4 *>(smem + kP + pds_chunk(i, 2 * gi)) = make_uint4(pb[0], pb[1], pb[2], pb[3]);
         *reinterpret_cast<uint4 *>(smem + kP + pds_chunk(i, 2 * gi + 1)) = make_uint4(pb[4], pb[5], pb[6], pb[7]);
       };
@@ -1460,7 +1502,8 @@ bool tensor_maps(TmaSet *t, const void *base, const Geo &g) {
 int launch_fwd_tc(const FwdArgs &a, void *stream) {
   TmaSet mq, mk, mv;
   if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g)) return SWIN_ERR_CUDA;
-  auto kern = a.g.pack == 2 ? fwd::fwd_tc_kernel<2> : fwd::fwd_tc_kernel<1>;
+  auto kern = a.drop.thr ? (a.g.pack == 2 ? fwd::fwd_tc_kernel<2, true> : fwd::fwd_tc_kernel<1, true>)
+                         : (a.g.pack == 2 ? fwd::fwd_tc_kernel<2, false> : fwd::fwd_tc_kernel<1, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::kSmemBytes) != cudaSuccess)
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, fwd::kThreads, fwd::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mk, mv);
@@ -1472,7 +1515,8 @@ int launch_bwd_tc(const BwdArgs &a, void *stream) {
   if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g) ||
       !tensor_maps(&mdo, a.dout, a.g))
     return SWIN_ERR_CUDA;
-  auto kern = a.g.pack == 2 ? bwd::bwd_tc_kernel<2> : bwd::bwd_tc_kernel<1>;
+  auto kern = a.drop.thr ? (a.g.pack == 2 ? bwd::bwd_tc_kernel<2, true> : bwd::bwd_tc_kernel<1, true>)
+                         : (a.g.pack == 2 ? bwd::bwd_tc_kernel<2, false> : bwd::bwd_tc_kernel<1, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::kSmemBytes) != cudaSuccess)
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, bwd::kThreads, bwd::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mk, mv, mdo);

@@ -1,0 +1,130 @@
+"""Dropout from a counter-based generator: no mask is ever stored.
+
+A decision is a pure function of (seed, step, site, index), so the backward
+recomputes what the forward drew. The seed and the step live on the device in
+a ``DropoutState``; the kernels read them when they run, so a captured step
+replays with the step it finds there. A training step uses one state for all
+its dropouts, each with a site of its own, and advances the state once its
+backward is done.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import swin_attn as C
+
+_C_DTYPE = {torch.bfloat16: C.SWIN_BF16, torch.float32: C.SWIN_F32}
+
+
+class DropoutState:
+    """Seed (64 bits) and step of the generator, as an int64 CUDA tensor of two."""
+
+    def __init__(self, seed, step=0, device=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if not 0 <= int(seed) < 2 ** 64:
+            raise ValueError("seed: a whole number of 64 bits, got %r" % (seed,))
+        seed = int(seed) - (2 ** 64 if int(seed) >= 2 ** 63 else 0)
+        self.tensor = torch.tensor([seed, int(step)], dtype=torch.int64, device=device)
+
+    def advance(self, steps=1):
+        """Go on to the next training step (on the current stream; may be
+        captured). Between a forward and its backward it is an error, which
+        autograd reports."""
+        self.tensor[1:].add_(steps)
+
+
+class Dropout:
+    """One dropout of a model: its rate, its site and the state it draws from.
+
+    The rate takes effect as T / 65536, T = round(rate * 65536); what is kept
+    is scaled by 1 / (1 - T / 65536). Dropouts of one step need different
+    sites, or they drop the same positions.
+    """
+
+    def __init__(self, state, rate, site):
+        if not isinstance(state, DropoutState):
+            raise ValueError("state: expected a DropoutState, got %s" % type(state).__name__)
+        if not (0.0 <= rate < 1.0) or round(rate * 65536) > 65535:
+            raise ValueError("rate: from 0 to 65535/65536, got %r" % (rate,))
+        if int(site) != site or not 0 <= site < 2 ** 32:
+            raise ValueError("site: a whole number of 32 bits, got %r" % (site,))
+        self.state, self.rate, self.site = state, float(rate), int(site)
+        self.desc = C.swin_attn_drop(self.rate, self.site, state.tensor.data_ptr())
+
+    @property
+    def active(self):
+        return round(self.rate * 65536) > 0
+
+
+def check_dropout(name, drop, device):
+    if not isinstance(drop, Dropout):
+        raise ValueError("%s: expected a Dropout, got %s" % (name, type(drop).__name__))
+    if drop.state.tensor.device != device:
+        raise ValueError("%s: its state is on %s, expected %s" % (name, drop.state.tensor.device, device))
+
+
+class on:
+    """Make `device` (and `stream`, if given) current while outputs are
+    allocated and the call is issued, so that what the call allocates belongs
+    to the stream that uses it."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError("stream: on %s, the tensors are on %s" % (stream.device, device))
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def apply_dropout(x, drop, span=1, out=None, stream=None):
+    """y_i = x_i / kept where decision i // span keeps, else 0 (i: position in
+    the contiguous x). span = 1: dropout; tokens * channels: whole images
+    (stochastic depth). The backward is the same call on the gradient. `out`
+    may be x. drop = None copies."""
+    from .functional import check_tensor
+    if not isinstance(x, torch.Tensor) or x.dtype not in _C_DTYPE:
+        raise ValueError("x: expected a bfloat16 or float32 torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError("x: on %s, expected a CUDA device" % x.device)
+    check_tensor("x", x, x.shape, x.dtype, x.device)
+    if int(span) != span or span < 1:
+        raise ValueError("span: at least 1, got %r" % (span,))
+    if drop is not None:
+        check_dropout("drop", drop, x.device)
+    if out is not None:
+        check_tensor("out", out, x.shape, x.dtype, x.device)
+    with on(x.device, stream):
+        out = torch.empty_like(x) if out is None else out
+        C.swin_attn_dropout(_C_DTYPE[x.dtype], x.numel(), int(span), x, drop.desc if drop else None, out, stream)
+    return out
+
+
+class _DropoutFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, drop, span):
+        ctx.drop, ctx.span = drop, span
+        if drop is not None:
+            ctx.save_for_backward(drop.state.tensor)  # a state advanced before the backward is reported
+        return apply_dropout(x.contiguous(), drop, span)
+
+    @staticmethod
+    def backward(ctx, dy):
+        ctx.saved_tensors
+        return apply_dropout(dy.contiguous(), ctx.drop, ctx.span), None, None
+
+
+def dropout(x, drop, span=1):
+    """Autograd-aware dropout (see apply_dropout)."""
+    return _DropoutFn.apply(x, drop, span)

@@ -8,6 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import swin_attn as C
+from .dropout import check_dropout
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 
@@ -93,19 +94,34 @@ class SwinWindowAttention:
     def new_bias(self):
         return torch.zeros((self.info.bias_rows, self.heads), dtype=torch.float32, device=self.device)
 
-    def forward(self, q, k, v, bias=None, land=None, o=None, lse=None, need_lse=True, stream=None):
+    def _check_dropout(self, dropout):
+        """The dropout's descriptor, or None where it drops nothing."""
+        if dropout is None:
+            return None
+        check_dropout("dropout", dropout, self.device)
+        return dropout.desc if dropout.active else None
+
+    def forward(self, q, k, v, bias=None, land=None, o=None, lse=None, need_lse=True, stream=None, dropout=None):
+        """(O, log-sum-exp). `dropout` (a Dropout) drops softmax probabilities."""
+        drop = self._check_dropout(dropout)
         self._check(q=q, k=k, v=v, bias=bias, land=land, o=o, lse=lse)
         if o is None:
             o = torch.empty(self.shape, dtype=self.torch_dtype, device=self.device)
         if lse is None and need_lse:
             lse = torch.empty(self.lse_shape, dtype=torch.float32, device=self.device)
-        C.swin_attn_fwd(self.plan, q, k, v, bias, land if self.has_land else None, o, lse, stream)
+        land = land if self.has_land else None
+        if drop is None:
+            C.swin_attn_fwd(self.plan, q, k, v, bias, land, o, lse, stream)
+        else:
+            C.swin_attn_fwd_dropout(self.plan, q, k, v, bias, land, o, lse, drop, stream)
         return o, lse
 
     def backward(self, q, k, v, dout, lse, bias=None, land=None, dq=None, dk=None, dv=None, dbias=None,
-                 want_dbias=True, stream=None, o=None):
+                 want_dbias=True, stream=None, o=None, dropout=None):
         """Gradients (dq, dk, dv, dbias). With the forward's output `o`, head_dim
-        128 takes delta = dout . o instead of recomputing it (one key sweep less)."""
+        128 takes delta = dout . o instead of recomputing it (one key sweep less).
+        `dropout` is the forward's, its state not advanced since."""
+        drop = self._check_dropout(dropout)
         if lse is None:
             raise ValueError("lse: the backward needs the forward's log-sum-exp")
         self._check(q=q, k=k, v=v, dout=dout, lse=lse, bias=bias, land=land, dq=dq, dk=dk, dv=dv, dbias=dbias,
@@ -116,7 +132,10 @@ class SwinWindowAttention:
         if dbias is None and want_dbias:
             dbias = self.new_bias()
         ws = self.workspace()  # dBias partial tables; for head_dim 128 also delta
-        if o is None:
+        if drop is not None:
+            C.swin_attn_bwd_dropout(self.plan, q, k, v, o, dout, lse, bias, land if self.has_land else None, dq, dk, dv,
+                                    dbias, ws, drop, stream)
+        elif o is None:
             C.swin_attn_bwd(self.plan, q, k, v, dout, lse, bias, land if self.has_land else None, dq, dk, dv, dbias,
                             ws, stream)
         else:
@@ -146,25 +165,27 @@ class SwinWindowAttention:
 
 class _SwinAttnFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, attn, q, k, v, bias, land):
+    def forward(ctx, attn, q, k, v, bias, land, dropout):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-        o, lse = attn.forward(q, k, v, bias, land)
-        ctx.attn = attn
-        ctx.save_for_backward(q, k, v, bias, land, lse, o)
+        o, lse = attn.forward(q, k, v, bias, land, dropout=dropout)
+        ctx.attn, ctx.dropout = attn, dropout
+        # the dropout's state is saved so that one advanced before the backward is reported
+        ctx.save_for_backward(q, k, v, bias, land, lse, o, None if dropout is None else dropout.state.tensor)
         return o
 
     @staticmethod
     def backward(ctx, dout):
-        q, k, v, bias, land, lse, o = ctx.saved_tensors
+        q, k, v, bias, land, lse, o, _ = ctx.saved_tensors
         want_dbias = bias is not None and ctx.needs_input_grad[4]
         dq, dk, dv, dbias = ctx.attn.backward(q, k, v, dout.contiguous(), lse, bias, land, want_dbias=want_dbias,
-                                              o=o)
-        return None, dq, dk, dv, dbias, None
+                                              o=o, dropout=ctx.dropout)
+        return None, dq, dk, dv, dbias, None, None
 
 
-def swin_window_attention(attn: SwinWindowAttention, q, k, v, bias=None, land=None):
-    """Autograd-aware SW-MSA: returns O; gradients flow to q, k, v and bias."""
-    return _SwinAttnFn.apply(attn, q, k, v, bias, land)
+def swin_window_attention(attn: SwinWindowAttention, q, k, v, bias=None, land=None, dropout=None):
+    """Autograd-aware SW-MSA: returns O; gradients flow to q, k, v and bias.
+    `dropout` (a Dropout) drops softmax probabilities."""
+    return _SwinAttnFn.apply(attn, q, k, v, bias, land, dropout)
 
 
 class SwinBlockPair:

@@ -37,6 +37,9 @@ SWIN_BF16 = 1
 SWIN_IMPL_AUTO = 0
 SWIN_IMPL_SIMT = 1
 SWIN_IMPL_TC = 2
+SWIN_NORM_NONE = 0
+SWIN_NORM_LAYER = 1
+SWIN_NORM_RMS = 2
 
 
 class SwinAttnError(RuntimeError):
@@ -58,6 +61,30 @@ class swin_attn_plan_info(ctypes.Structure):
                 ("slots", ctypes.c_int32), ("bias_rows", ctypes.c_int32), ("impl", ctypes.c_int32),
                 ("fwd_ctas", ctypes.c_int32), ("bwd_ctas", ctypes.c_int32), ("num_sms", ctypes.c_int32),
                 ("work_items", ctypes.c_int64), ("dbias_slots", ctypes.c_int64)]
+
+
+class swin_attn_drop(ctypes.Structure):
+    _fields_ = [("rate", ctypes.c_double), ("site", ctypes.c_uint32), ("state", ctypes.c_void_p)]
+
+
+class swin_attn_norm(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("gamma", ctypes.c_void_p),
+                ("beta", ctypes.c_void_p)]
+
+
+class swin_attn_rows(ctypes.Structure):
+    _fields_ = [("images", ctypes.c_int64), ("tokens", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class swin_attn_join(ctypes.Structure):
+    _fields_ = [("post", swin_attn_norm), ("pre", swin_attn_norm), ("scale", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("drop", swin_attn_drop), ("path", swin_attn_drop)]
+
+
+class swin_attn_join_grads(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("post_gamma", "post_beta", "scale", "gate", "pre_gamma",
+                                                     "pre_beta")]
 
 
 _lib = None
@@ -87,6 +114,24 @@ def load_library():
     lib.swin_attn_bwd.restype = ctypes.c_int
     lib.swin_attn_bwd_o.argtypes = [vp] * 14 + [sz, vp]
     lib.swin_attn_bwd_o.restype = ctypes.c_int
+    lib.swin_attn_fwd_dropout.argtypes = [vp] * 8 + [ctypes.POINTER(swin_attn_drop), vp]
+    lib.swin_attn_fwd_dropout.restype = ctypes.c_int
+    lib.swin_attn_bwd_dropout.argtypes = [vp] * 14 + [sz, ctypes.POINTER(swin_attn_drop), vp]
+    lib.swin_attn_bwd_dropout.restype = ctypes.c_int
+    rows, norm, join = (ctypes.POINTER(t) for t in (swin_attn_rows, swin_attn_norm, swin_attn_join))
+    lib.swin_attn_rows_workspace_bytes.argtypes = [rows]
+    lib.swin_attn_rows_workspace_bytes.restype = sz
+    lib.swin_attn_norm_fwd.argtypes = [rows, vp, norm, vp, vp]
+    lib.swin_attn_norm_fwd.restype = ctypes.c_int
+    lib.swin_attn_norm_bwd.argtypes = [rows, vp, norm, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.swin_attn_norm_bwd.restype = ctypes.c_int
+    lib.swin_attn_join_fwd.argtypes = [rows, vp, vp, join, vp, vp, vp]
+    lib.swin_attn_join_fwd.restype = ctypes.c_int
+    lib.swin_attn_join_bwd.argtypes = [rows, vp, vp, join, vp, vp, vp, vp, ctypes.POINTER(swin_attn_join_grads), vp,
+                                       sz, vp]
+    lib.swin_attn_join_bwd.restype = ctypes.c_int
+    lib.swin_attn_dropout.argtypes = [i32, i64, i64, vp, ctypes.POINTER(swin_attn_drop), vp, vp]
+    lib.swin_attn_dropout.restype = ctypes.c_int
     lib.swin_attn_bwd_noalloc.argtypes = [vp] * 13
     lib.swin_attn_bwd_noalloc.restype = ctypes.c_int
     lib.swin_attn_block_fwd.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -253,6 +298,63 @@ def swin_attn_bwd_o(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, d
                                           _ptr(land, 4, "land"), pdq, pdk, pdv, _ptr(dbias, 4, "dbias"),
                                           _ptr(workspace, 256, "workspace"), ws_bytes, _stream(stream)),
            "swin_attn_bwd_o")
+
+
+def swin_attn_fwd_dropout(plan: Plan, q, k, v, bias, land, o, lse, drop: swin_attn_drop, stream=None) -> None:
+    pq, pk, pv, po, plse = _acts(("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse))
+    _check(load_library().swin_attn_fwd_dropout(plan.handle, pq, pk, pv, _ptr(bias, 4, "bias"),
+                                                _ptr(land, 4, "land"), po, plse, drop, _stream(stream)),
+           "swin_attn_fwd_dropout")
+
+
+def swin_attn_bwd_dropout(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace,
+                          drop: swin_attn_drop, stream=None) -> None:
+    """Backward with the forward's dropout (the same site, rate and an unchanged state)."""
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    pq, pk, pv, po, pdo, plse, pdq, pdk, pdv = _acts(("q", q), ("k", k), ("v", v), ("o", o), ("dout", dout),
+                                                     ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv))
+    _check(load_library().swin_attn_bwd_dropout(plan.handle, pq, pk, pv, po, pdo, plse, _ptr(bias, 4, "bias"),
+                                                _ptr(land, 4, "land"), pdq, pdk, pdv, _ptr(dbias, 4, "dbias"),
+                                                _ptr(workspace, 256, "workspace"), ws_bytes, drop, _stream(stream)),
+           "swin_attn_bwd_dropout")
+
+
+def swin_attn_rows_workspace_bytes(rows: swin_attn_rows) -> int:
+    return int(load_library().swin_attn_rows_workspace_bytes(rows))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def swin_attn_norm_fwd(rows: swin_attn_rows, x, norm: swin_attn_norm, h, stream=None) -> None:
+    _check(load_library().swin_attn_norm_fwd(rows, _addr(x), norm, _addr(h), _stream(stream)), "swin_attn_norm_fwd")
+
+
+def swin_attn_norm_bwd(rows: swin_attn_rows, x, norm: swin_attn_norm, dh, dres, dx, dgamma, dbeta, workspace,
+                       stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().swin_attn_norm_bwd(rows, _addr(x), norm, _addr(dh), _addr(dres), _addr(dx), _addr(dgamma),
+                                             _addr(dbeta), _addr(workspace), ws_bytes, _stream(stream)),
+           "swin_attn_norm_bwd")
+
+
+def swin_attn_join_fwd(rows: swin_attn_rows, x, z, join: swin_attn_join, y, h, stream=None) -> None:
+    _check(load_library().swin_attn_join_fwd(rows, _addr(x), _addr(z), join, _addr(y), _addr(h), _stream(stream)),
+           "swin_attn_join_fwd")
+
+
+def swin_attn_join_bwd(rows: swin_attn_rows, y, z, join: swin_attn_join, dy, dh, dx, dz, grads: swin_attn_join_grads,
+                       workspace, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().swin_attn_join_bwd(rows, _addr(y), _addr(z), join, _addr(dy), _addr(dh), _addr(dx),
+                                             _addr(dz), grads, _addr(workspace), ws_bytes, _stream(stream)),
+           "swin_attn_join_bwd")
+
+
+def swin_attn_dropout(dtype: int, n: int, span: int, x, drop: swin_attn_drop, y, stream=None) -> None:
+    _check(load_library().swin_attn_dropout(dtype, n, span, _addr(x), drop, _addr(y), _stream(stream)),
+           "swin_attn_dropout")
 
 
 def swin_attn_bwd_noalloc(plan: Plan, q, k, v, dout, lse, bias, land, dq, dk, dv, dbias, stream=None) -> None:
