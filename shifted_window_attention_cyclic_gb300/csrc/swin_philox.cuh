@@ -73,12 +73,79 @@ struct Philox {
     }
     return make_uint4(c0, c1, c2, c3);
   }
+
+  // N blocks, a round of all at a time: independent chains (a wide multiply
+  // issues every fourth cycle at best, and a lone chain waits for each).
+  template <int N>
+  __device__ __forceinline__ void blocks(const uint64_t (&b)[N], uint4 (&u)[N]) const {
+    uint32_t a = k0, k = k1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = make_uint4((uint32_t)b[i], (uint32_t)(b[i] >> 32), site, step);
+#pragma unroll
+    for (int r = 0; r < 7; ++r) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t p0 = (uint64_t)u[i].x * 0xD2511F53u, p1 = (uint64_t)u[i].z * 0xCD9E8D57u;
+        u[i] = make_uint4((uint32_t)(p1 >> 32) ^ u[i].y ^ a, (uint32_t)p1, (uint32_t)(p0 >> 32) ^ u[i].w ^ k, (uint32_t)p0);
+      }
+      a += 0x9E3779B9u;
+      k += 0xBB67AE85u;
+    }
+  }
 };
 
-// Decision e (a compile-time 0..7 after unrolling) of a block.
+// Decision e (a compile-time 0..7 after unrolling) of a block. The number is
+// compared in a word's upper half, where T << 16 sits: the odd ones as they
+// are (their lower half cannot change the outcome), the even ones moved up.
 __device__ __forceinline__ bool keep_of(const uint4 &u, int e, uint32_t thr) {
   const uint32_t w = e < 2 ? u.x : e < 4 ? u.y : e < 6 ? u.z : u.w;
-  return ((e & 1) ? (w >> 16) : (w & 0xFFFFu)) >= thr;
+  return ((e & 1) ? w : w << 16) >= thr << 16;
+}
+
+// Both decisions of a generator word at once, as the sign bits of its halves
+// (the other bits are not defined): with 15-bit values, u + (0x8000 - T) carries
+// into bit 15 iff u >= T. For T <= 0x8000 a number with its own top bit set
+// keeps whatever the rest; above, only such a number can keep.
+struct PairTest {
+  uint32_t add, any;
+  __device__ __forceinline__ void init(uint32_t thr) {
+    any = thr <= 0x8000u ? ~0u : 0u;
+    add = (0x8000u - (thr <= 0x8000u ? thr : thr - 0x8000u)) * 0x10001u;
+  }
+  __device__ __forceinline__ uint32_t signs(uint32_t w) const {
+    const uint32_t t = (w & 0x7FFF7FFFu) + add;
+    return (t & w) | (any & (t | w));
+  }
+};
+
+// The decisions of a 16-key group (two generator blocks) as four bits in each
+// byte: key 4 k + j at bit k of byte j. The signs of four halves become four
+// bytes of ones or zeros in one byte permute (selectors that replicate a sign),
+// so two words cost one permute and one LOP.
+__device__ __forceinline__ uint32_t group_bits(const uint4 &a, const uint4 &b, const PairTest &test) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t bits = 0u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t m;
+    asm("prmt.b32 %0, %1, %2, 0xFDB9;" : "=r"(m) : "r"(test.signs(w[2 * k])), "r"(test.signs(w[2 * k + 1])));
+    bits |= m & (0x01010101u << k);
+  }
+  return bits;
+}
+// 0xFFFF in the halves that keep, 0 in the others, of keys e and e + 1 (e even) of
+// the group whose bits start at bit `at` (0 or 4) of the word's bytes.
+__device__ __forceinline__ uint32_t keep_mask(uint32_t word, int at, int e) {
+  uint32_t m;
+  if (e & 2)
+    asm("prmt.b32 %0, %1, 0, 0xBBAA;" : "=r"(m) : "r"(word << (7 - at - (e >> 2))));
+  else
+    asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m) : "r"(word << (7 - at - (e >> 2))));
+  return m;
+}
+// Key e of that group alone.
+__device__ __forceinline__ bool keep_bit(uint32_t word, int at, int e) {
+  return (word & (1u << (8 * (e & 3) + at + (e >> 2)))) != 0u;
 }
 
 // A block's eight decisions, bit e = decision e keeps.

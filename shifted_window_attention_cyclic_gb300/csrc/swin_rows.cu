@@ -56,6 +56,11 @@ struct RowArgs {
 };
 
 // ---- eight channels of a row -----------------------------------------------
+// A vector is 8 channels: 16 bytes of bf16, 32 of fp32. In registers it is four
+// float2, the operands of the packed fp32 instructions (two results an issue).
+template <typename T>
+constexpr int vec_bytes() { return 8 * (int)sizeof(T); }
+
 template <typename T>
 struct Raw;
 template <>
@@ -67,43 +72,28 @@ struct Raw<float> {
   float4 a, b;
 };
 
-template <typename T>
-__device__ __forceinline__ Raw<T> load8(const void *base, int64_t vec);
-template <>
-__device__ __forceinline__ Raw<__nv_bfloat16> load8<__nv_bfloat16>(const void *base, int64_t vec) {
-  return {static_cast<const uint4 *>(base)[vec]};
-}
-template <>
-__device__ __forceinline__ Raw<float> load8<float>(const void *base, int64_t vec) {
-  const float4 *p = static_cast<const float4 *>(base) + 2 * vec;
-  return {p[0], p[1]};
-}
-
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16> &r, float (&f)[8]) {
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16> &r, float2 (&f)[4]) {
   const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = __uint_as_float(w[e] << 16);
-    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-  }
+  for (int e = 0; e < 4; ++e) f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack(const Raw<float> &r, float (&f)[8]) {
-  f[0] = r.a.x, f[1] = r.a.y, f[2] = r.a.z, f[3] = r.a.w;
-  f[4] = r.b.x, f[5] = r.b.y, f[6] = r.b.z, f[7] = r.b.w;
+__device__ __forceinline__ void unpack(const Raw<float> &r, float2 (&f)[4]) {
+  f[0] = make_float2(r.a.x, r.a.y), f[1] = make_float2(r.a.z, r.a.w);
+  f[2] = make_float2(r.b.x, r.b.y), f[3] = make_float2(r.b.z, r.b.w);
 }
 
-__device__ __forceinline__ void pack(const float (&f)[8], Raw<__nv_bfloat16> &r) {
+__device__ __forceinline__ void pack(const float2 (&f)[4], Raw<__nv_bfloat16> &r) {
   uint32_t w[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[e].x, f[e].y);
     w[e] = *reinterpret_cast<const uint32_t *>(&h);
   }
   r.v = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void pack(const float (&f)[8], Raw<float> &r) {
-  r.a = make_float4(f[0], f[1], f[2], f[3]);
-  r.b = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void pack(const float2 (&f)[4], Raw<float> &r) {
+  r.a = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  r.b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
 
 __device__ __forceinline__ void store8(void *base, int64_t vec, const Raw<__nv_bfloat16> &r) {
@@ -116,103 +106,191 @@ __device__ __forceinline__ void store8(void *base, int64_t vec, const Raw<float>
 }
 
 // Per-channel fp32 parameters of this thread's channels (absent: `none`).
-__device__ __forceinline__ void load_param(const float *p, int vec, bool ok, float none, float (&f)[8]) {
+__device__ __forceinline__ void load_param(const float *p, int vec, bool ok, float none, float2 (&f)[4]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = p && ok ? __ldg(p + 8 * vec + e) : none;
+  for (int e = 0; e < 4; ++e)
+    f[e] = p && ok ? make_float2(__ldg(p + 8 * vec + 2 * e), __ldg(p + 8 * vec + 2 * e + 1)) : make_float2(none, none);
 }
 
-// ---- sums over a row ---------------------------------------------------------
-// K sums over the TPR threads of a row. Rows of up to 32 threads stay inside a
-// warp; wider rows are the whole CTA and exchange one value per warp through
-// one of two shared buffers (used in turn: one barrier per sum).
-template <int TPR, int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float *xchg, int &turn) {
-#pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
-    float *buf = xchg + turn * (2 * W);
-    turn ^= 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < K; ++k) buf[k * W + warp] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) s += buf[k * W + w];
-      v[k] = s;
-    }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+// Pair e (0..3) of a vector where the decisions of its generator block keep, else 0.
+__device__ __forceinline__ float2 kept(const uint4 &bits, int e, uint32_t thr, float2 v) {
+  return make_float2(keep_of(bits, 2 * e, thr) ? v.x : 0.f, keep_of(bits, 2 * e + 1, thr) ? v.y : 0.f);
+}
+
+// ---- the ring ------------------------------------------------------------------
+// Rows come through a ring of D + 1 stages in shared memory, D rows ahead, by
+// 16-byte asynchronous copies (cp.async). Every thread copies exactly the
+// vectors that it reads back, so the ring needs no barrier, only the thread's
+// own wait for its copies; the bytes in flight no longer depend on how many
+// registers a warp's work takes.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Slot (stage, tensor, vector j) of this thread: 16-byte pieces of consecutive
+// threads are consecutive (no bank conflicts).
+template <typename T, int kThreads, int NT, int NV>
+struct Ring {
+  static constexpr int kPieces = vec_bytes<T>() / 16;
+  static constexpr int kStage = kThreads * NT * NV * vec_bytes<T>();
+  uint8_t *base;
+  uint32_t addr;
+  __device__ __forceinline__ void init(uint8_t *smem) {
+    base = smem + threadIdx.x * 16;
+    addr = static_cast<uint32_t>(__cvta_generic_to_shared(base));
   }
-}
+  static __device__ __forceinline__ int slot(int stage, int t, int j) {
+    return stage * kStage + (t * NV + j) * kPieces * kThreads * 16;
+  }
+  // a vector of a tensor (its first byte's place if it is not there: nothing is read, zeros arrive)
+  __device__ __forceinline__ void fetch(int stage, int t, int j, const void *tensor, int64_t vec, bool there) const {
+    const uint8_t *src = static_cast<const uint8_t *>(tensor) + (there ? vec * vec_bytes<T>() : 0);
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) copy16(addr + slot(stage, t, j) + p * kThreads * 16, src + 16 * p, there);
+  }
+  __device__ __forceinline__ void read(int stage, int t, int j, float2 (&f)[4]) const {
+    const uint8_t *p = base + slot(stage, t, j);
+    Raw<T> r;
+    if constexpr (kPieces == 1) {
+      r.v = *reinterpret_cast<const uint4 *>(p);
+    } else {
+      r.a = *reinterpret_cast<const float4 *>(p);
+      r.b = *reinterpret_cast<const float4 *>(p + kThreads * 16);
+    }
+    unpack(r, f);
+  }
+};
 
+// ---- launch shapes ----------------------------------------------------------------
+// One kernel's shape: TPR threads a row with NV vectors each, NT input tensors.
 constexpr int block_of(int tpr) { return tpr > 32 ? tpr : 256; }
 
-// Mean and 1 / deviation of up to two rows at once (u with norm kind ku, v
-// with kv; kind NONE leaves that row alone). inv = 1 / C.
-template <int TPR, int NV, int K>
-__device__ __forceinline__ void row_stats(const float (&u)[K][NV][8], const bool (&ok)[NV], const int (&kind)[K],
-                                          const float (&eps)[K], float inv, float (&mean)[K], float (&rstd)[K],
-                                          float *xchg, int &turn) {
-  bool any_mean = false;
+// Resident CTAs an SM (and the register bound that allows them). Backward: four
+// column sums, two parameters and four rows of 8 channels are 80 registers
+// before any address, so 512 threads with 128 registers; twice that for two
+// vectors.
+constexpr int blocks_per_sm(int tpr, int nv, bool bwd) {
+  return bwd ? (nv == 2 ? 1 : 512 / block_of(tpr)) : (nv == 2 ? 512 : 768) / block_of(tpr);
+}
+
+// Rows ahead: 64 KB in flight on an SM cover HBM's latency at its rate (about
+// 1 us at 45 GB/s a SM), as far as 200 KB of shared memory hold the ring.
+constexpr int rows_ahead(int stage_bytes, int blocks) {
+  int d = (65536 + blocks * stage_bytes - 1) / (blocks * stage_bytes);
+  const int most = 200 * 1024 / blocks / stage_bytes - 1;
+  d = d > most ? most : d;
+  return d < 0 ? 0 : d > 7 ? 7 : d;
+}
+
+template <typename T, int TPR, int NV, bool kBwd, bool kBranch, bool kPre>
+struct Shape {
+  static constexpr int threads = block_of(TPR);
+  static constexpr int blocks = blocks_per_sm(TPR, NV, kBwd);
+  static constexpr int tensors = kBwd ? 1 + (kPre ? 2 : 0) + (kBranch ? 1 : 0) : (kBranch ? 2 : 1);
+  static constexpr int stage = threads * tensors * NV * vec_bytes<T>();
+  static constexpr int ahead = rows_ahead(stage, blocks);
+  static constexpr int flush = kBwd && TPR <= 32 ? threads * NV * 32 : 0;
+  static constexpr int smem = (ahead + 1) * stage > flush ? (ahead + 1) * stage : flush;
+  static_assert(smem <= 227 * 1024, "over a CTA's shared memory");
+};
+
+// ---- sums over a row ---------------------------------------------------------
+// Sums of a pair over the TPR threads of a row. Rows of up to 32 threads stay
+// inside a warp; wider rows are the whole CTA and exchange one pair per warp
+// through one of two shared buffers (used in turn: one barrier per sum).
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float2 v, float2 *xchg, int &turn) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    mean[k] = 0.f;
-    any_mean = any_mean || kind[k] == SWIN_NORM_LAYER;
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+    v = add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float2 *buf = xchg + turn * W;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = buf[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v = add(v, buf[w]);
   }
-  if (any_mean) {
-    float s[K];
+  return v;
+}
+
+template <int NV>
+__device__ __forceinline__ float sum_of(const float2 (&u)[NV][4]) {
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      s[k] = 0.f;
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
+    for (int e = 0; e < 4; ++e) s = add(s, u[j][e]);
+  return s.x + s.y;
+}
+template <int NV>
+__device__ __forceinline__ float dot_of(const float2 (&u)[NV][4], const float2 (&v)[NV][4]) {
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[k] += u[k][j][e];
-    }
-    row_sum<TPR, K>(s, xchg, turn);
+  for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int k = 0; k < K; ++k) mean[k] = kind[k] == SWIN_NORM_LAYER ? s[k] * inv : 0.f;
+    for (int e = 0; e < 4; ++e) s = fma(u[j][e], v[j][e], s);
+  return s.x + s.y;
+}
+// u - m; vectors past the row's end stay 0
+template <int NV>
+__device__ __forceinline__ void centre(float2 (&u)[NV][4], float m, const bool (&ok)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const float2 n = both(ok[j] ? -m : 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[j][e] = add(u[j][e], n);
   }
-  float q[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    q[k] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = ok[j] ? u[k][j][e] - mean[k] : 0.f;
-        q[k] = fmaf(d, d, q[k]);
-      }
-  }
-  row_sum<TPR, K>(q, xchg, turn);
-#pragma unroll
-  for (int k = 0; k < K; ++k) rstd[k] = 1.0f / sqrtf(fmaf(q[k], inv, eps[k]));
+}
+
+// Where a CTA's rows lie and which of them a thread works on.
+struct Place {
+  int lane, sub;
+  int64_t first, stride;
+};
+template <int TPR>
+__device__ __forceinline__ Place place() {
+  constexpr int kWarps = block_of(TPR) / 32, RPW = TPR < 32 ? 32 / TPR : 1;  // rows a warp works on at once
+  Place p;
+  p.lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
+  p.sub = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
+  p.first = TPR > 32 ? 0 : (threadIdx.x >> 5) * RPW;
+  p.stride = TPR > 32 ? 1 : kWarps * RPW;
+  return p;
 }
 
 // ---- forward -----------------------------------------------------------------
 template <typename T, int TPR, int NV, bool kBranch, bool kPre>
-__global__ void __launch_bounds__(block_of(TPR)) rows_fwd_kernel(const RowArgs a) {
-  constexpr int kThreads = block_of(TPR), kWarps = kThreads / 32;
-  constexpr int RPW = TPR < 32 ? 32 / TPR : 1;  // rows a warp works on at once
-  __shared__ float xchg[TPR > 32 ? 4 * (TPR / 32) : 1];
+__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false)) rows_fwd_kernel(const RowArgs a) {
+  using S = Shape<T, TPR, NV, false, kBranch, kPre>;
+  constexpr int D = S::ahead;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
   int turn = 0;
-  const int lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
+  const Place pl = place<TPR>();
   const int C8 = a.C >> 3;
   const float inv = 1.0f / (float)a.C;
+  Ring<T, S::threads, S::tensors, NV> ring;
+  ring.init(smem);
   bool ok[NV];
-  float gpre[NV][8], bpre[NV][8], wg[NV][8], wb[NV][8];
+  float2 gpre[NV][4], bpre[NV][4], wg[NV][4], wb[NV][4];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    ok[j] = j * TPR + lane < C8;
+    ok[j] = j * TPR + pl.lane < C8;
     if constexpr (kPre) {
-      load_param(a.pre.gamma, j * TPR + lane, ok[j], 1.f, gpre[j]);
-      load_param(a.pre.beta, j * TPR + lane, ok[j], 0.f, bpre[j]);
+      load_param(a.pre.gamma, j * TPR + pl.lane, ok[j], 1.f, gpre[j]);
+      load_param(a.pre.beta, j * TPR + pl.lane, ok[j], 0.f, bpre[j]);
     }
   }
   Philox ph;
@@ -221,83 +299,103 @@ __global__ void __launch_bounds__(block_of(TPR)) rows_fwd_kernel(const RowArgs a
 
   const int64_t L = (int64_t)blockIdx.x * a.chunk;
   const int64_t R = min(L + a.chunk, a.rows);
-  const int64_t stride = TPR > 32 ? 1 : (int64_t)kWarps * RPW;
-  const int64_t first = TPR > 32 ? 0 : (threadIdx.x >> 5) * RPW;
-  const int sub = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
   // one image of the CTA's rows at a time: the gate and the path decision change with it
   for (int64_t s = L; s < R;) {
     const int64_t b = s / a.tokens;
     const int64_t e1 = min(R, (b + 1) * a.tokens);
+    auto fetch = [&](int64_t r0, int stage) {
+      const int64_t row = r0 + pl.sub, vec0 = row * C8 + pl.lane;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const bool there = ok[j] && row < e1;
+        ring.fetch(stage, 0, j, a.x, vec0 + j * TPR, there);
+        if constexpr (kBranch) ring.fetch(stage, 1, j, a.z, vec0 + j * TPR, there);
+      }
+      copies_commit();
+    };
+    int64_t ahead = s + pl.first;
+    int in = 0, out = 0;
+#pragma unroll
+    for (int k = 0; k < D; ++k, ahead += pl.stride) fetch(ahead, in++);
+    bool path = true;
     if constexpr (kBranch) {
-      float path = a.drop.thr ? a.drop.scale : 1.f;
+      float c = a.drop.scale;  // what is kept is multiplied by, with the gate and the layer scale
       if (a.path.thr) {
         Philox pp;
         pp.init(a.path);
-        path = keep_one(pp, (uint64_t)b, a.path.thr) ? path * a.path.scale : 0.f;
+        path = keep_one(pp, (uint64_t)b, a.path.thr);
+        c *= a.path.scale;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        float t[8];
-        load_param(a.scale, j * TPR + lane, ok[j], 1.f, wg[j]);
-        load_param(a.gate ? a.gate + b * a.C : nullptr, j * TPR + lane, ok[j], 1.f, t);
+        float2 t[4];
+        load_param(a.scale, j * TPR + pl.lane, ok[j], 1.f, wg[j]);
+        load_param(a.gate ? a.gate + b * a.C : nullptr, j * TPR + pl.lane, ok[j], 1.f, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wb[j][e] = wg[j][e] = wg[j][e] * t[e] * path;
-        load_param(a.post.gamma, j * TPR + lane, ok[j] && post, 1.f, t);
+        for (int e = 0; e < 4; ++e) wb[j][e] = wg[j][e] = mul(mul(wg[j][e], t[e]), both(c));
+        load_param(a.post.gamma, j * TPR + pl.lane, ok[j] && post, 1.f, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wg[j][e] *= t[e];
-        load_param(a.post.beta, j * TPR + lane, ok[j] && post, 0.f, t);
+        for (int e = 0; e < 4; ++e) wg[j][e] = mul(wg[j][e], t[e]);
+        load_param(a.post.beta, j * TPR + pl.lane, ok[j] && post, 0.f, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) wb[j][e] *= t[e];
+        for (int e = 0; e < 4; ++e) wb[j][e] = mul(wb[j][e], t[e]);
       }
     }
-    for (int64_t r0 = s + first; r0 < e1; r0 += stride) {
-      const int64_t row = r0 + sub;
+    for (int64_t r0 = s + pl.first; r0 < e1; r0 += pl.stride, ahead += pl.stride) {
+      fetch(ahead, in);
+      in = in == D ? 0 : in + 1;
+      copies_wait<D>();
+      const int64_t row = r0 + pl.sub;
       const bool live = row < e1;
-      const int64_t vec0 = row * C8 + lane;
-      float v[1][NV][8], u[1][NV][8];
+      const int64_t vec0 = row * C8 + pl.lane;
+      float2 v[NV][4];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        Raw<T> rx = {}, rz = {};
-        if (ok[j] && live) {
-          rx = load8<T>(a.x, vec0 + j * TPR);
-          if constexpr (kBranch) rz = load8<T>(a.z, vec0 + j * TPR);
-        }
-        unpack(rx, v[0][j]);
-        unpack(rz, u[0][j]);
-      }
+      for (int j = 0; j < NV; ++j) ring.read(out, 0, j, v[j]);
       if constexpr (kBranch) {
-        float mean[1] = {0.f}, rstd[1] = {1.f};
-        if (post) row_stats<TPR, NV, 1>(u, ok, {a.post.kind}, {a.post.eps}, inv, mean, rstd, xchg, turn);
+        float2 u[NV][4];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) ring.read(out, 1, j, u[j]);
+        float2 rstd = both(1.f);
+        if (post) {
+          if (a.post.kind == SWIN_NORM_LAYER)
+            centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
+          rstd = both(rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.post.eps)));
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          uint4 bits = make_uint4(~0u, ~0u, ~0u, ~0u);
-          if (a.drop.thr) bits = ph.block((uint64_t)(vec0 + j * TPR));
+          if (path) {  // a dropped image's y is x
+            uint4 bits;
+            if (a.drop.thr) bits = ph.block((uint64_t)(vec0 + j * TPR));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float hat = post ? (u[0][j][e] - mean[0]) * rstd[0] : u[0][j][e];
-            const float br = fmaf(hat, wg[j][e], wb[j][e]);
-            v[0][j][e] += keep_of(bits, e, a.drop.thr) ? br : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              float2 br = fma(mul(u[j][e], rstd), wg[j][e], wb[j][e]);
+              if (a.drop.thr) br = kept(bits, e, a.drop.thr, br);
+              v[j][e] = add(v[j][e], br);
+            }
           }
-          Raw<T> out;
-          pack(v[0][j], out);
-          if (ok[j] && live) store8(a.y, vec0 + j * TPR, out);
-          unpack(out, v[0][j]);  // h is the norm of y as stored
+          Raw<T> o;
+          pack(v[j], o);
+          if (ok[j] && live) store8(a.y, vec0 + j * TPR, o);
+          if constexpr (kPre) unpack(o, v[j]);  // h is the norm of y as stored
         }
       }
+      out = out == D ? 0 : out + 1;
       if constexpr (kPre) {
-        float mean[1], rstd[1];
-        row_stats<TPR, NV, 1>(v, ok, {a.pre.kind}, {a.pre.eps}, inv, mean, rstd, xchg, turn);
+        if (a.pre.kind == SWIN_NORM_LAYER)
+          centre<NV>(v, row_sum<TPR>(make_float2(sum_of<NV>(v), 0.f), xchg, turn).x * inv, ok);
+        const float2 rstd =
+            both(rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(v, v), 0.f), xchg, turn).x, inv, a.pre.eps)));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          float o[8];
+          Raw<T> o;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = fmaf((v[0][j][e] - mean[0]) * rstd[0], gpre[j][e], bpre[j][e]);
-          Raw<T> out;
-          pack(o, out);
-          if (ok[j] && live) store8(a.h, vec0 + j * TPR, out);
+          for (int e = 0; e < 4; ++e) v[j][e] = fma(mul(v[j][e], rstd), gpre[j][e], bpre[j][e]);
+          pack(v[j], o);
+          if (ok[j] && live) store8(a.h, vec0 + j * TPR, o);
         }
       }
     }
+    copies_wait<0>();
     s = e1;
   }
 }
@@ -305,29 +403,22 @@ __global__ void __launch_bounds__(block_of(TPR)) rows_fwd_kernel(const RowArgs a
 // ---- backward ----------------------------------------------------------------
 // Sums the CTA's copies of this thread's channels and writes them: dst[C].
 template <int TPR, int NV>
-__device__ __forceinline__ void flush(float (&acc)[NV][8], float *dst, int C8, float *buf) {
+__device__ __forceinline__ void flush(float2 (&acc)[NV][4], float *dst, int C8, float *buf) {
   constexpr int kThreads = block_of(TPR);
   const int lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
+  auto put = [&](float *p, const float2 (&v)[4]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  };
   if constexpr (TPR > 32) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int v = j * TPR + lane;
-      if (v < C8) {
-        float4 *p = reinterpret_cast<float4 *>(dst + 8 * v);
-        p[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-        p[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
-      }
-    }
+    for (int j = 0; j < NV; ++j)
+      if (j * TPR + lane < C8) put(dst + 8 * (j * TPR + lane), acc[j]);
   } else {
     constexpr int G = kThreads / TPR, W = TPR * NV * 8;  // rows in flight, channels of a row (padded)
-    const int g = threadIdx.x / TPR;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float4 *p = reinterpret_cast<float4 *>(buf + g * W + 8 * (j * TPR + lane));
-      p[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      p[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
-    }
+    for (int j = 0; j < NV; ++j) put(buf + threadIdx.x / TPR * W + 8 * (j * TPR + lane), acc[j]);
     __syncthreads();
     for (int c = threadIdx.x; c < 8 * C8; c += kThreads) {
       float s = 0.f;
@@ -339,30 +430,31 @@ __device__ __forceinline__ void flush(float (&acc)[NV][8], float *dst, int C8, f
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) acc[j][e] = make_float2(0.f, 0.f);
 }
 
 template <typename T, int TPR, int NV, bool kBranch, bool kPre>
-__global__ void __launch_bounds__(block_of(TPR)) rows_bwd_kernel(const RowArgs a) {
-  constexpr int kThreads = block_of(TPR), kWarps = kThreads / 32;
-  constexpr int RPW = TPR < 32 ? 32 / TPR : 1;
-  constexpr int K = (kBranch ? 1 : 0) + (kPre ? 1 : 0);  // rows with statistics
-  constexpr int kZ = 0, kY = kBranch ? 1 : 0;            // their indexes
-  __shared__ float xchg[TPR > 32 ? 4 * (TPR / 32) : 1];
-  __shared__ __align__(16) float buf[TPR > 32 ? 4 : kThreads * NV * 8];
+__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) rows_bwd_kernel(const RowArgs a) {
+  using S = Shape<T, TPR, NV, true, kBranch, kPre>;
+  constexpr int D = S::ahead;
+  constexpr int tDy = 0, tY = 1, tDh = 2, tZ = kPre ? 3 : 1;  // tensors of a stage
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
   int turn = 0;
-  const int lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
+  const Place pl = place<TPR>();
   const int C8 = a.C >> 3;
   const float inv = 1.0f / (float)a.C;
+  Ring<T, S::threads, S::tensors, NV> ring;
+  ring.init(smem);
   bool ok[NV];
-  float gpre[NV][8], w[NV][8];
-  float a1[NV][8], a0[NV][8], b1[NV][8], b0[NV][8];  // column sums: dh yhat, dh; G zhat, G
+  float2 gpre[NV][4], w[NV][4];
+  float2 a1[NV][4], a0[NV][4], b1[NV][4], b0[NV][4];  // column sums: dh yhat, dh; G zhat, G
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    ok[j] = j * TPR + lane < C8;
-    if constexpr (kPre) load_param(a.pre.gamma, j * TPR + lane, ok[j], 1.f, gpre[j]);
+    ok[j] = j * TPR + pl.lane < C8;
+    if constexpr (kPre) load_param(a.pre.gamma, j * TPR + pl.lane, ok[j], 1.f, gpre[j]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a1[j][e] = a0[j][e] = b1[j][e] = b0[j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) a1[j][e] = a0[j][e] = b1[j][e] = b0[j][e] = make_float2(0.f, 0.f);
   }
   Philox ph;
   ph.init(a.drop);
@@ -370,138 +462,167 @@ __global__ void __launch_bounds__(block_of(TPR)) rows_bwd_kernel(const RowArgs a
 
   const int64_t L = (int64_t)blockIdx.x * a.chunk;
   const int64_t R = min(L + a.chunk, a.rows);
-  const int64_t stride = TPR > 32 ? 1 : (int64_t)kWarps * RPW;
-  const int64_t first = TPR > 32 ? 0 : (threadIdx.x >> 5) * RPW;
-  const int sub = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
   for (int64_t s = L; s < R;) {
     const int64_t b = s / a.tokens;
     const int64_t e1 = min(R, (b + 1) * a.tokens);
-    float path = 1.f;  // kept values' scale times the image's path factor
+    auto fetch = [&](int64_t r0, int stage) {
+      const int64_t row = r0 + pl.sub, vec0 = row * C8 + pl.lane;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const bool there = ok[j] && row < e1;
+        if (a.dy) ring.fetch(stage, tDy, j, a.dy, vec0 + j * TPR, there);
+        if constexpr (kPre) {
+          ring.fetch(stage, tY, j, a.x, vec0 + j * TPR, there);
+          ring.fetch(stage, tDh, j, a.dh, vec0 + j * TPR, there);
+        }
+        if constexpr (kBranch)
+          if (a.z) ring.fetch(stage, tZ, j, a.z, vec0 + j * TPR, there);
+      }
+      copies_commit();
+    };
+    int64_t ahead = s + pl.first;
+    int in = 0, out = 0;
+#pragma unroll
+    for (int k = 0; k < D; ++k, ahead += pl.stride) fetch(ahead, in++);
+    bool path = true;
     if constexpr (kBranch) {
-      path = a.drop.thr ? a.drop.scale : 1.f;
+      float c = a.drop.scale;  // the kept values' scales: in dz here, in the column sums at the fold
       if (a.path.thr) {
         Philox pp;
         pp.init(a.path);
-        path = keep_one(pp, (uint64_t)b, a.path.thr) ? path * a.path.scale : 0.f;
+        path = keep_one(pp, (uint64_t)b, a.path.thr);
+        c *= a.path.scale;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        float t[8];
-        load_param(a.scale, j * TPR + lane, ok[j], 1.f, w[j]);
-        load_param(a.gate ? a.gate + b * a.C : nullptr, j * TPR + lane, ok[j], 1.f, t);
+        float2 t[4];
+        load_param(a.scale, j * TPR + pl.lane, ok[j], 1.f, w[j]);
+        load_param(a.gate ? a.gate + b * a.C : nullptr, j * TPR + pl.lane, ok[j], 1.f, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[j][e] *= t[e];
-        load_param(a.post.gamma, j * TPR + lane, ok[j] && post, 1.f, t);
+        for (int e = 0; e < 4; ++e) w[j][e] = mul(mul(w[j][e], t[e]), both(c));
+        load_param(a.post.gamma, j * TPR + pl.lane, ok[j] && post, 1.f, t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[j][e] *= t[e];
+        for (int e = 0; e < 4; ++e) w[j][e] = mul(w[j][e], t[e]);
       }
     }
-    for (int64_t r0 = s + first; r0 < e1; r0 += stride) {
-      const int64_t row = r0 + sub;
-      const bool live = row < e1;
-      const int64_t vec0 = row * C8 + lane;
-      float u[K][NV][8], g[NV][8], dh[NV][8];  // z and y rows; dy; dh
+    for (int64_t r0 = s + pl.first; r0 < e1; r0 += pl.stride, ahead += pl.stride) {
+      fetch(ahead, in);
+      in = in == D ? 0 : in + 1;
+      copies_wait<D>();
+      const int64_t row = r0 + pl.sub;
+      const bool live = row < e1;  // rows past the end arrived as zeros and add nothing to the sums
+      const int64_t vec0 = row * C8 + pl.lane;
+      float2 g[NV][4];  // dy, then dy' = dx
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        Raw<T> ry = {}, rz = {}, rg = {}, rh = {};
-        if (ok[j] && live) {
-          if constexpr (kPre) {
-            ry = load8<T>(a.x, vec0 + j * TPR);
-            if (a.dh) rh = load8<T>(a.dh, vec0 + j * TPR);
-          }
-          if constexpr (kBranch)
-            if (a.z) rz = load8<T>(a.z, vec0 + j * TPR);
-          if (a.dy) rg = load8<T>(a.dy, vec0 + j * TPR);
+        if (a.dy) {
+          ring.read(out, tDy, j, g[j]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[j][e] = make_float2(0.f, 0.f);
         }
-        if constexpr (kBranch) unpack(rz, u[kZ][j]);
-        if constexpr (kPre) unpack(ry, u[kY][j]);
-        unpack(rg, g[j]);
-        unpack(rh, dh[j]);
       }
-      float mean[K], rstd[K];
-      int kind[K];
-      float eps[K];
-      if constexpr (kBranch) kind[kZ] = a.post.kind, eps[kZ] = post ? a.post.eps : 1.f;
-      if constexpr (kPre) kind[kY] = a.pre.kind, eps[kY] = a.pre.eps;
-      if (kPre || post)
-        row_stats<TPR, NV, K>(u, ok, kind, eps, inv, mean, rstd, xchg, turn);
       if constexpr (kPre) {
-        float c[2] = {0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float hat = ok[j] ? (u[kY][j][e] - mean[kY]) * rstd[kY] : 0.f;
-            u[kY][j][e] = hat;
-            a1[j][e] = fmaf(dh[j][e], live ? hat : 0.f, a1[j][e]);
-            a0[j][e] += dh[j][e];
-            dh[j][e] *= gpre[j][e];
-            c[0] += dh[j][e];
-            c[1] = fmaf(dh[j][e], hat, c[1]);
-          }
-        row_sum<TPR, 2>(c, xchg, turn);
-        const float c0 = a.pre.kind == SWIN_NORM_LAYER ? c[0] * inv : 0.f, c1 = c[1] * inv;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            g[j][e] = fmaf(rstd[kY], dh[j][e] - fmaf(u[kY][j][e], c1, c0), g[j][e]);
-      }
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        Raw<T> out;
-        pack(g[j], out);
-        if (ok[j] && live) store8(a.dx, vec0 + j * TPR, out);
-      }
-      if constexpr (kBranch) {
-        float c[2] = {0.f, 0.f};
+        float2 u[NV][4], dh[NV][4];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          uint4 bits = make_uint4(~0u, ~0u, ~0u, ~0u);
+          ring.read(out, tY, j, u[j]);
+          ring.read(out, tDh, j, dh[j]);
+        }
+        const bool layer = a.pre.kind == SWIN_NORM_LAYER;
+        if (layer) centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
+        const float rstd = rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.pre.eps));
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            u[j][e] = mul(u[j][e], both(rstd));
+            a1[j][e] = fma(dh[j][e], u[j][e], a1[j][e]);
+            a0[j][e] = add(a0[j][e], dh[j][e]);
+            dh[j][e] = mul(dh[j][e], gpre[j][e]);
+          }
+        const float2 c = row_sum<TPR>(make_float2(dot_of<NV>(dh, u), layer ? sum_of<NV>(dh) : 0.f), xchg, turn);
+        const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            g[j][e] = fma(both(rstd), add(dh[j][e], fma(u[j][e], c1, c0)), g[j][e]);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        Raw<T> o;
+        pack(g[j], o);
+        if (ok[j] && live) store8(a.dx, vec0 + j * TPR, o);
+      }
+      if constexpr (kBranch) {
+        float2 u[NV][4];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (a.z && path) {
+            ring.read(out, tZ, j, u[j]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[j][e] = make_float2(0.f, 0.f);
+          }
+        }
+        const bool layer = a.post.kind == SWIN_NORM_LAYER;
+        float rstd = 1.f;
+        if (layer) centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
+        if (post) rstd = rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.post.eps));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const bool in_row = ok[j] && live;  // past the row's end dy' is not 0
+          uint4 bits;
           if (a.drop.thr) bits = ph.block((uint64_t)(vec0 + j * TPR));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float gd = keep_of(bits, e, a.drop.thr) && ok[j] && live ? g[j][e] * path : 0.f;
-            const float hat = !ok[j] || !live ? 0.f : post ? (u[kZ][j][e] - mean[kZ]) * rstd[kZ] : u[kZ][j][e];
-            u[kZ][j][e] = hat;
-            b1[j][e] = fmaf(gd, hat, b1[j][e]);
-            b0[j][e] += gd;
-            g[j][e] = gd * w[j][e];
-            c[0] += g[j][e];
-            c[1] = fmaf(g[j][e], hat, c[1]);
+          for (int e = 0; e < 4; ++e) {
+            u[j][e] = mul(u[j][e], both(rstd));
+            if (!path || !in_row) g[j][e] = make_float2(0.f, 0.f);
+            if (a.drop.thr) {
+              g[j][e] = kept(bits, e, a.drop.thr, g[j][e]);
+              // what was dropped takes no part, were it infinite (a row's norm has it in its statistics anyway)
+              if (!post) u[j][e] = kept(bits, e, a.drop.thr, u[j][e]);
+            }
+            b1[j][e] = fma(g[j][e], u[j][e], b1[j][e]);
+            b0[j][e] = add(b0[j][e], g[j][e]);
+            g[j][e] = mul(g[j][e], w[j][e]);
           }
         }
         if (post) {
-          row_sum<TPR, 2>(c, xchg, turn);
-          const float c0 = a.post.kind == SWIN_NORM_LAYER ? c[0] * inv : 0.f, c1 = c[1] * inv;
+          const float2 c = row_sum<TPR>(make_float2(dot_of<NV>(g, u), layer ? sum_of<NV>(g) : 0.f), xchg, turn);
+          const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[j][e] = rstd[kZ] * (g[j][e] - fmaf(u[kZ][j][e], c1, c0));
+            for (int e = 0; e < 4; ++e) g[j][e] = mul(both(rstd), add(g[j][e], fma(u[j][e], c1, c0)));
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          Raw<T> out;
-          pack(g[j], out);
-          if (ok[j] && live) store8(a.dz, vec0 + j * TPR, out);
+          Raw<T> o;
+          pack(g[j], o);
+          if (ok[j] && live) store8(a.dz, vec0 + j * TPR, o);
         }
       }
+      out = out == D ? 0 : out + 1;
     }
+    copies_wait<0>();
     // with a gate the sums are kept per image: slot CTA + image (a CTA's next
     // image takes its next slot, the next CTA's first is one further)
     if constexpr (kBranch)
       if (a.part_post && (a.gate || e1 == R)) {
         float *dst = a.part_post + ((int64_t)blockIdx.x + (a.gate ? b : 0)) * 2 * a.C;
-        flush<TPR, NV>(b1, dst, C8, buf);
-        flush<TPR, NV>(b0, dst + a.C, C8, buf);
+        flush<TPR, NV>(b1, dst, C8, reinterpret_cast<float *>(smem));
+        flush<TPR, NV>(b0, dst + a.C, C8, reinterpret_cast<float *>(smem));
+        if (TPR <= 32) __syncthreads();  // the ring takes the buffer again
       }
     s = e1;
   }
   if constexpr (kPre)
     if (a.part_pre) {
       float *dst = a.part_pre + (int64_t)blockIdx.x * 2 * a.C;
-      flush<TPR, NV>(a1, dst, C8, buf);
-      flush<TPR, NV>(a0, dst + a.C, C8, buf);
+      flush<TPR, NV>(a1, dst, C8, reinterpret_cast<float *>(smem));
+      flush<TPR, NV>(a0, dst + a.C, C8, reinterpret_cast<float *>(smem));
     }
 }
 
@@ -510,6 +631,7 @@ struct ColArgs {
   int64_t tokens, chunk, rows;
   int images, C, ctas;
   bool post_norm;
+  float kept;  // what kept values are multiplied by (left out of the join's sums)
   const float *part_pre, *part_post;
   const float *scale, *gate, *gamma, *beta;  // gamma, beta: the post norm's
   float *dpre_gamma, *dpre_beta, *dpost_gamma, *dpost_beta, *dscale, *dgate;
@@ -548,8 +670,8 @@ __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a
         v1 += a.part_post[s * C2 + cc];
         v0 += a.part_post[s * C2 + a.C + cc];
       }
-    v1 = lane_sum(v1, buf);
-    v0 = lane_sum(v0, buf);
+    v1 = a.kept * lane_sum(v1, buf);
+    v0 = a.kept * lane_sum(v0, buf);
     if (own) {
       const float gm = a.post_norm && a.gamma ? a.gamma[c] : 1.f, bt = a.post_norm && a.beta ? a.beta[c] : 0.f;
       a.dgate[b * a.C + c] = (a.scale ? a.scale[c] : 1.f) * fmaf(gm, v1, bt * v0);
@@ -591,8 +713,8 @@ __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a
         v0 += a.part_post[s * C2 + a.C + cc];
       }
     }
-    v1 = lane_sum(v1, buf);
-    v0 = lane_sum(v0, buf);
+    v1 = a.kept * lane_sum(v1, buf);
+    v0 = a.kept * lane_sum(v0, buf);
     if (own) {
       const float sc = a.scale ? a.scale[c] : 1.f;
       const float gm = a.post_norm && a.gamma ? a.gamma[c] : 1.f, bt = a.post_norm && a.beta ? a.beta[c] : 0.f;
@@ -617,13 +739,19 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
     uint4 bits = make_uint4(0u, 0u, 0u, 0u);
     if (kMode == 0) bits = ph.block((uint64_t)v);
     if (kMode == 1 && keep_one(ph, (uint64_t)(i0 / span), d.thr)) bits = make_uint4(~0u, ~0u, ~0u, ~0u);
-    float f[8];
     if (i0 + 8 <= n) {
-      unpack(load8<T>(x, v), f);
+      const Raw<T> in = *reinterpret_cast<const Raw<T> *>(x + i0);
+      float2 f[4];
+      unpack(in, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool keep = kMode == 2 ? keep_one(ph, (uint64_t)((i0 + e) / span), d.thr) : keep_of(bits, e, d.thr);
-        f[e] = keep ? f[e] * d.scale : 0.f;
+      for (int e = 0; e < 4; ++e) {
+        f[e] = mul(f[e], both(d.scale));
+        if (kMode == 2) {
+          f[e].x = keep_one(ph, (uint64_t)((i0 + 2 * e) / span), d.thr) ? f[e].x : 0.f;
+          f[e].y = keep_one(ph, (uint64_t)((i0 + 2 * e + 1) / span), d.thr) ? f[e].y : 0.f;
+        } else {
+          f[e] = kept(bits, e, d.thr, f[e]);
+        }
       }
       Raw<T> out;
       pack(f, out);
@@ -639,23 +767,23 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
   }
 }
 
-// ---- launch shapes ---------------------------------------------------------------
-struct Shape {
-  int tpr, nv, ctas_per_sm;
+// ---- launches ----------------------------------------------------------------------
+struct Width {
+  int tpr, nv;
 };
 
 // Threads per row and vectors per thread: the narrowest that holds the row.
-Shape shape_of(int C) {
+Width width_of(int C) {
   const int c8 = C >> 3;
-  if (c8 <= 4) return {4, 1, 2};
-  if (c8 <= 8) return {8, 1, 2};
-  if (c8 <= 16) return {16, 1, 2};
-  if (c8 <= 32) return {32, 1, 2};
-  if (c8 <= 64) return {32, 2, 1};
-  if (c8 <= 128) return {128, 1, 4};
-  if (c8 <= 256) return {256, 1, 2};
-  if (c8 <= 512) return {256, 2, 1};
-  return {512, 2, 1};
+  if (c8 <= 4) return {4, 1};
+  if (c8 <= 8) return {8, 1};
+  if (c8 <= 16) return {16, 1};
+  if (c8 <= 32) return {32, 1};
+  if (c8 <= 64) return {32, 2};
+  if (c8 <= 128) return {128, 1};
+  if (c8 <= 256) return {256, 1};
+  if (c8 <= 512) return {256, 2};
+  return {512, 2};
 }
 
 struct Split {
@@ -663,11 +791,12 @@ struct Split {
   int ctas;
 };
 
-Split split_rows(int64_t rows, int C, int sms, int per_sm) {
-  const Shape sh = shape_of(C);
-  const int64_t at_once = sh.tpr > 32 ? 1 : 256 / sh.tpr;
+// Consecutive rows per CTA, as many CTAs as fit on the GPU at once.
+Split split_rows(int64_t rows, int C, int sms, bool bwd) {
+  const Width wd = width_of(C);
+  const int64_t at_once = wd.tpr > 32 ? 1 : 256 / wd.tpr;
   const int64_t groups = (rows + at_once - 1) / at_once;
-  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)sms * per_sm));
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)sms * blocks_per_sm(wd.tpr, wd.nv, bwd)));
   int64_t chunk = (rows + ctas - 1) / ctas;
   chunk = std::max<int64_t>(1, (chunk + at_once - 1) / at_once * at_once);
   return {chunk, (int)((rows + chunk - 1) / chunk)};
@@ -681,32 +810,42 @@ int sm_count(int *sms) {
   return SWIN_OK;
 }
 
-template <typename T, int TPR, int NV>
-int launch_rows(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
-  constexpr int t = block_of(TPR);
-  if (bwd) {
-    if (branch && pre) rows_bwd_kernel<T, TPR, NV, true, true><<<ctas, t, 0, st>>>(a);
-    else if (branch) rows_bwd_kernel<T, TPR, NV, true, false><<<ctas, t, 0, st>>>(a);
-    else rows_bwd_kernel<T, TPR, NV, false, true><<<ctas, t, 0, st>>>(a);
-  } else {
-    if (branch && pre) rows_fwd_kernel<T, TPR, NV, true, true><<<ctas, t, 0, st>>>(a);
-    else if (branch) rows_fwd_kernel<T, TPR, NV, true, false><<<ctas, t, 0, st>>>(a);
-    else rows_fwd_kernel<T, TPR, NV, false, true><<<ctas, t, 0, st>>>(a);
-  }
+template <typename T, int TPR, int NV, bool kBwd, bool kBranch, bool kPre>
+int launch_one(const RowArgs &a, int ctas, cudaStream_t st) {
+  using S = Shape<T, TPR, NV, kBwd, kBranch, kPre>;
+  void (*kern)(const RowArgs);
+  if constexpr (kBwd) kern = rows_bwd_kernel<T, TPR, NV, kBranch, kPre>;
+  else kern = rows_fwd_kernel<T, TPR, NV, kBranch, kPre>;
+  if (S::smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess)
+    return SWIN_ERR_CUDA;
+  kern<<<ctas, S::threads, S::smem, st>>>(a);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }
 
+template <typename T, int TPR, int NV>
+int launch_rows(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
+  if (bwd) {
+    if (branch && pre) return launch_one<T, TPR, NV, true, true, true>(a, ctas, st);
+    if (branch) return launch_one<T, TPR, NV, true, true, false>(a, ctas, st);
+    return launch_one<T, TPR, NV, true, false, true>(a, ctas, st);
+  }
+  if (branch && pre) return launch_one<T, TPR, NV, false, true, true>(a, ctas, st);
+  if (branch) return launch_one<T, TPR, NV, false, true, false>(a, ctas, st);
+  return launch_one<T, TPR, NV, false, false, true>(a, ctas, st);
+}
+
 template <typename T>
-int launch_shape(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
-  const Shape sh = shape_of(a.C);
-  if (sh.tpr == 4) return launch_rows<T, 4, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 8) return launch_rows<T, 8, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 16) return launch_rows<T, 16, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 32 && sh.nv == 1) return launch_rows<T, 32, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 32) return launch_rows<T, 32, 2>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 128) return launch_rows<T, 128, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 256 && sh.nv == 1) return launch_rows<T, 256, 1>(a, bwd, branch, pre, ctas, st);
-  if (sh.tpr == 256) return launch_rows<T, 256, 2>(a, bwd, branch, pre, ctas, st);
+int launch_width(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
+  const Width wd = width_of(a.C);
+  if (wd.tpr == 4) return launch_rows<T, 4, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 8) return launch_rows<T, 8, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 16) return launch_rows<T, 16, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 32 && wd.nv == 1) return launch_rows<T, 32, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 32) return launch_rows<T, 32, 2>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 128) return launch_rows<T, 128, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 256 && wd.nv == 1) return launch_rows<T, 256, 1>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 256) return launch_rows<T, 256, 2>(a, bwd, branch, pre, ctas, st);
   return launch_rows<T, 512, 2>(a, bwd, branch, pre, ctas, st);
 }
 
@@ -756,7 +895,7 @@ size_t swin_attn_rows_workspace_bytes(const swin_attn_rows *r) {
   size_t bytes = 0;
   int sms = 0;
   if (check_rows(r, &rows, &bytes) || sm_count(&sms)) return 0;
-  const Split sp = split_rows(rows, r->channels, sms, shape_of(r->channels).ctas_per_sm);
+  const Split sp = split_rows(rows, r->channels, sms, true);
   const size_t need = ((size_t)sp.ctas + (size_t)col_slots(sp.ctas, r->images)) * 2 * r->channels * sizeof(float);
   return (need + 255) & ~size_t(255);
 }
@@ -782,11 +921,11 @@ int swin_attn_norm_fwd(const swin_attn_rows *r, const void *x, const swin_attn_n
   a.images = 1;
   a.C = r->channels;
   a.path.scale = a.drop.scale = 1.f;
-  const Split sp = split_rows(a.rows, a.C, sms, 4 * shape_of(a.C).ctas_per_sm);
+  const Split sp = split_rows(a.rows, a.C, sms, false);
   a.chunk = sp.chunk;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return r->dtype == SWIN_BF16 ? launch_shape<__nv_bfloat16>(a, false, false, true, sp.ctas, st)
-                               : launch_shape<float>(a, false, false, true, sp.ctas, st);
+  return r->dtype == SWIN_BF16 ? launch_width<__nv_bfloat16>(a, false, false, true, sp.ctas, st)
+                               : launch_width<float>(a, false, false, true, sp.ctas, st);
 }
 
 int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, const swin_attn_join *join, void *y,
@@ -819,11 +958,11 @@ int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, co
   a.tokens = r->tokens;
   a.images = (int)r->images;
   a.C = r->channels;
-  const Split sp = split_rows(a.rows, a.C, sms, 4 * shape_of(a.C).ctas_per_sm);
+  const Split sp = split_rows(a.rows, a.C, sms, false);
   a.chunk = sp.chunk;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return r->dtype == SWIN_BF16 ? launch_shape<__nv_bfloat16>(a, false, true, pre, sp.ctas, st)
-                               : launch_shape<float>(a, false, true, pre, sp.ctas, st);
+  return r->dtype == SWIN_BF16 ? launch_width<__nv_bfloat16>(a, false, true, pre, sp.ctas, st)
+                               : launch_width<float>(a, false, true, pre, sp.ctas, st);
 }
 
 }  // extern "C"
@@ -842,7 +981,7 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   a.C = r->channels;
   a.images = (int)r->images;
   a.tokens = branch ? r->tokens : a.rows;  // the norm alone does not look at images
-  const Split sp = split_rows(a.rows, a.C, sms, shape_of(a.C).ctas_per_sm);
+  const Split sp = split_rows(a.rows, a.C, sms, true);
   a.chunk = sp.chunk;
   if (want_pre || want_post) {
     if (!workspace || workspace_bytes < swin_attn_rows_workspace_bytes(r)) return SWIN_ERR_WORKSPACE;
@@ -852,8 +991,8 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
     a.part_post = want_post ? ws + (size_t)sp.ctas * 2 * a.C : nullptr;
   }
   if (a.rows) {
-    rc = r->dtype == SWIN_BF16 ? launch_shape<__nv_bfloat16>(a, true, branch, pre, sp.ctas, st)
-                               : launch_shape<float>(a, true, branch, pre, sp.ctas, st);
+    rc = r->dtype == SWIN_BF16 ? launch_width<__nv_bfloat16>(a, true, branch, pre, sp.ctas, st)
+                               : launch_width<float>(a, true, branch, pre, sp.ctas, st);
     if (rc) return rc;
   }
   if (!want_pre && !want_post) return SWIN_OK;
@@ -865,6 +1004,7 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   c.C = a.C;
   c.ctas = a.rows ? sp.ctas : 0;
   c.post_norm = post;
+  c.kept = a.drop.scale * a.path.scale;
   c.part_pre = a.part_pre;
   c.part_post = a.part_post;
   c.scale = a.scale;

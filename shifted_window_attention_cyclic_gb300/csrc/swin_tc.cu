@@ -483,6 +483,43 @@ __device__ __forceinline__ void gather_role(const Geo &g, const StageLayout &lay
   }
 }
 
+// Dropout decisions of a softmax thread's half row (its warpgroup's keys, in
+// 16-key groups from its first): group k has its bits (group_bits) in word k / 2,
+// at bits 4 * (k % 2) of the bytes.
+struct KeepDraw {
+  Philox ph;
+  PairTest test;
+  int nb, first;  // generator blocks of a row's keys; the half row's first
+  __device__ __forceinline__ void init(const Geo &g, const Drop &d, int first_block) {
+    ph.init(d);
+    test.init(d.thr);
+    nb = (g.n + 7) >> 3;
+    first = first_block;
+  }
+  // One group, two generator blocks, a trip of a rolled loop: on the 256 x 540
+  // stage (16 heads, 96 slots) the forward takes 351 us and the backward 572 us,
+  // against 216 and 448 us without dropout (of the difference, 20 and 60 us are
+  // the use of the bits). The roles' code together is larger than the
+  // instruction caches, so shorter code wins: two groups a trip took 390 / 588 us,
+  // unrolled by two 384 / 613 us, rolled rounds 408 / 613 us, drawn beside the
+  // exponentials 348 / 650 us. Drawn by the epilogue warps, one bit per key
+  // through shared memory, it took 351 / 608 us (those warps have no idle time),
+  // by four more warps with the registers split over the roles 519 / 767 us.
+  __device__ __forceinline__ uint2 half_row(const Geo &g, const ItemCursor &x, int src, int groups) const {
+    uint64_t b = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + first;
+    uint2 w = make_uint2(0u, 0u);
+#pragma unroll 1
+    for (int k = 0; k < groups; ++k, b += 2) {
+      const uint64_t at[2] = {b, b + 1};
+      uint4 r[2];
+      ph.blocks(at, r);
+      const uint32_t bits = group_bits(r[0], r[1], test) << (4 * (k & 1));
+      if (k < 2) w.x |= bits; else w.y |= bits;
+    }
+    return w;
+  }
+};
+
 // ---------------------------------------------------------------- forward ---
 namespace fwd {
 
@@ -531,10 +568,9 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 
 // kPack: windows per work item (1 or 2), a compile-time copy per value so
 // that the one-window kernel carries no code for the second window.
-// kDrop: dropout of the probabilities. Thread (grp, i) draws the decisions of
-// its own row and keys beside the exponentials (one generator block per eight
-// keys), so no mask exists anywhere; the row sums are taken before it, and the
-// kept values' scale goes into the epilogue's 1 / l.
+// kDrop: dropout of the probabilities. A softmax thread draws its half row's
+// decisions while S is computed and ANDs them onto packed P; the row sums are
+// taken before, and the kept values' scale goes into the epilogue's 1 / l.
 template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_tc_kernel(const FwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
@@ -800,10 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h_last = count > 0 ? decode_item(g, R - 1).h : 0;  // heads rise by one along the range
     uint32_t bs_phase = 0;
     float *bvec = reinterpret_cast<float *>(smem + kBvec);
-    Philox ph;
-    if (kDrop) ph.init(a.drop);
-    const int nb = (g.n + 7) >> 3;                // generator blocks of a row's keys
-    const int kb0 = kPack == 2 ? 0 : 2 * gb;      // block of this thread's first key
+    KeepDraw draw;
+    if (kDrop) draw.init(g, a.drop, kPack == 2 ? 0 : 2 * gb);
     bool ok = true;
     if (a.debug_force_timeout && grp == 0) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     ItemCursor x;
@@ -837,6 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int wb = (int)(it & 1), xs = (int)(it % kXchgSlots);
       const uint32_t tS = tmem + lane_addr + kColS + 128u * wb;
+      uint2 keep = make_uint2(0u, 0u);  // this half row's decisions
+      if (kDrop && !idle) {
+        const int s = (int)(it % kStages);
+        if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
+        keep = draw.half_row(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i], ge - gb);
+      }
       if (!mbar_wait_warp(bar(bSFull + wb), (uint32_t)(it >> 1) & 1u, ctl)) break;
       tc_fence_after();
       if (idle) {
@@ -850,12 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive_warp(bar(bPFull + wb));
         continue;
-      }
-      uint64_t blk = 0;
-      if (kDrop) {  // the row's query token (the stage is held until this item's P is consumed)
-        if (!mbar_wait_warp(bar(bFull + (int)(it % kStages)), (uint32_t)(it / kStages) & 1u, ctl)) break;
-        const int src = reinterpret_cast<const int *>(smem + (int)(it % kStages) * kStageBytes + kMeta)[i];
-        blk = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + kb0;
       }
       uint32_t sv[4][16];
 #pragma unroll
@@ -892,19 +926,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k4 = 0; k4 < 4; ++k4) {
         if (gb + k4 < ge) {
           uint32_t pv[8];
-          uint4 bits = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const float2 xs2 =
                 __fadd2_rn(make_float2(__uint_as_float(sv[k4][e]), __uint_as_float(sv[k4][e + 1])), negm);
-            float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
+            const float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
             sp2[(e >> 1) & 3] = __fadd2_rn(sp2[(e >> 1) & 3], p);
-            if (kDrop) {
-              if ((e & 7) == 0) bits = ph.block(blk + 2 * k4 + (e >> 3));
-              p.x = keep_of(bits, e & 7, a.drop.thr) ? p.x : 0.f;
-              p.y = keep_of(bits, (e & 7) + 1, a.drop.thr) ? p.y : 0.f;
-            }
             pv[e >> 1] = pack_bf16(p.x, p.y);
+            if (kDrop) pv[e >> 1] &= keep_mask(k4 < 2 ? keep.x : keep.y, 4 * (k4 & 1), e);
           }
           tmem_st8(tS + 16u * (gb + k4), pv);  // over the first half of its own S group
         }
@@ -979,9 +1008,9 @@ __device__ __forceinline__ uint32_t pds_chunk(int i, int c) {
   return (c >> 3) * 16384 + (i >> 3) * 1024 + (i & 7) * 128 + (((c & 7) ^ (i & 7)) << 4);
 }
 
-// kDrop: pass 1 draws the forward's decisions again; a dropped key's dP is
-// zeroed where it lies in TMEM (pass 2 then needs no decisions) and its P in
-// the dV operand. The kept values' scale c is left out of both passes
+// kDrop: the softmax threads draw the forward's decisions again; a dropped key's
+// dP is zeroed where it lies in TMEM (pass 2 then needs no decisions) and its P
+// in the dV operand. The kept values' scale c is left out of both passes
 // (dS / c = P (keep dP - sum P keep dP)) and taken by the epilogue's multiplier
 // of dV, dK and dQ and by the dBias fold.
 template <int kPack, bool kDrop>
@@ -1205,10 +1234,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int cur_h = -1, h_first = -1;
     const int h_last = count > 0 ? decode_item(g, R - 1).h : 0;  // heads rise by one along the range
     uint32_t wsync_phase = 0;
-    Philox ph;
-    if (kDrop) ph.init(a.drop);
-    const int nb = (g.n + 7) >> 3;            // generator blocks of a row's keys
-    const int kg0 = kPack == 2 ? gb : 0;      // group that holds the row's window's first key
+    KeepDraw draw;
+    if (kDrop) draw.init(g, a.drop, kPack == 2 ? 0 : 2 * gb);
     bool ok = true;
     if (a.debug_force_timeout) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     // Fold the slot-pair dBias accumulator into bias rows (fixed order) and
@@ -1284,6 +1311,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur_h = x.h;
       }
       const int s = (int)(it % kStages);
+      uint2 keep = make_uint2(0u, 0u);  // this half row's decisions
+      if (kDrop && !idle) {
+        if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
+        keep = draw.half_row(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i], ge - gb);
+      }
       if (!mbar_wait_warp(bar(bSpFull), (uint32_t)it & 1u, ctl)) break;
       tc_fence_after();
       if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
@@ -1293,13 +1325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // pass 1: P = exp2(S*cs + bias2 - lse2); partial delta = sum_j P dP over
       // this half; P (fp32) back over S in TMEM, P (bf16) to the smem tile.
       float delta = 0.f;
-      uint64_t blk = 0;  // the row's first generator block
-      if (kDrop)
-        blk = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(reinterpret_cast<const int *>(sp + kMeta)[i], 0)) * nb;
       const float2 nl2 = make_float2(-lse2, -lse2);
-      auto p_group = [&](int gi, uint32_t (&sv)[16], uint32_t (&dpv)[16]) {
+      auto p_group = [&](int gi, uint32_t (&sv)[16], uint32_t (&dpv)[16], uint32_t kw, int at) {
         uint32_t pb[8];
-        uint4 bits = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int e4 = 0; e4 < 16; e4 += 4) {
           const float4 b4 = *reinterpret_cast<const float4 *>(brow + 16 * gi + e4);
@@ -1310,19 +1338,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    make_float2(bb[e - e4], bb[e - e4 + 1]));
             xs = __fadd2_rn(xs, nl2);
             const float p0 = live ? ex2(xs.x) : 0.f, p1 = live ? ex2(xs.y) : 0.f;
-            bool k0 = true, k1 = true;
             if (kDrop) {
-              if ((e & 7) == 0) bits = ph.block(blk + 2 * (gi - kg0) + (e >> 3));
-              k0 = keep_of(bits, e & 7, a.drop.thr);
-              k1 = keep_of(bits, (e & 7) + 1, a.drop.thr);
-              dpv[e] = k0 ? dpv[e] : 0u;
-              dpv[e + 1] = k1 ? dpv[e + 1] : 0u;
+              dpv[e] = keep_bit(kw, at, e) ? dpv[e] : 0u;
+              dpv[e + 1] = keep_bit(kw, at, e + 1) ? dpv[e + 1] : 0u;
             }
             delta = fmaf(p0, __uint_as_float(dpv[e]), delta);
             delta = fmaf(p1, __uint_as_float(dpv[e + 1]), delta);
             sv[e] = __float_as_uint(p0);  // P (fp32) overwrites S in the register buffer
             sv[e + 1] = __float_as_uint(p1);
-            pb[e >> 1] = pack_bf16(k0 ? p0 : 0.f, k1 ? p1 : 0.f);
+            pb[e >> 1] = pack_bf16(p0, p1);
+            if (kDrop) pb[e >> 1] &= keep_mask(kw, at, e);
           }
         }
         tmem_st16(tS + 16u * gi, sv);
@@ -1348,10 +1373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld16(tdP + 16u * g1, d1);
             }
             tmem_wait_ld_tied(s0, d0);
-            p_group(g0, s0, d0);
+            p_group(g0, s0, d0, k2 ? keep.y : keep.x, 0);
             if (g1 < ge) {
               tmem_tie(s1, d1);
-              p_group(g1, s1, d1);
+              p_group(g1, s1, d1, k2 ? keep.y : keep.x, 4);
             }
           }
         }
