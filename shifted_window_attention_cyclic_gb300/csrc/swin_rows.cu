@@ -52,6 +52,7 @@ struct RowArgs {
   Norm post, pre;
   const float *scale, *gate;
   Drop drop, path;
+  bool wide;                    // fp32 outputs lie on 32-byte boundaries
   float *part_pre, *part_post;  // column sums [ctas][2][C], [slots][2][C]; NULL: not wanted
 };
 
@@ -96,13 +97,37 @@ __device__ __forceinline__ void pack(const float2 (&f)[4], Raw<float> &r) {
   r.b = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
 }
 
-__device__ __forceinline__ void store8(void *base, int64_t vec, const Raw<__nv_bfloat16> &r) {
-  static_cast<uint4 *>(base)[vec] = r.v;
+// at byte `at` of a tensor. fp32: one 32-byte store where the tensor allows it;
+// two of 16 bytes leave half of every sector to the other (join forward, fp32,
+// 2 x 64 800 x 256: 130 us so, with halved loads too).
+__device__ __forceinline__ void store8(void *base, int64_t at, const Raw<__nv_bfloat16> &r, bool) {
+  *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(base) + at) = r.v;
 }
-__device__ __forceinline__ void store8(void *base, int64_t vec, const Raw<float> &r) {
-  float4 *p = static_cast<float4 *>(base) + 2 * vec;
-  p[0] = r.a;
-  p[1] = r.b;
+__device__ __forceinline__ void store8(void *base, int64_t at, const Raw<float> &r, bool wide) {
+  float4 *p = reinterpret_cast<float4 *>(static_cast<uint8_t *>(base) + at);
+  if (wide) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(r.a.x), "f"(r.a.y),
+                 "f"(r.a.z), "f"(r.a.w), "f"(r.b.x), "f"(r.b.y), "f"(r.b.z), "f"(r.b.w)
+                 : "memory");
+  } else {
+    p[0] = r.a;
+    p[1] = r.b;
+  }
+}
+
+__device__ __forceinline__ void load8(const void *p, Raw<__nv_bfloat16> &r, bool) {
+  r.v = *static_cast<const uint4 *>(p);
+}
+__device__ __forceinline__ void load8(const void *p, Raw<float> &r, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(r.a.x), "=f"(r.a.y), "=f"(r.a.z), "=f"(r.a.w), "=f"(r.b.x), "=f"(r.b.y), "=f"(r.b.z), "=f"(r.b.w)
+                 : "l"(p)
+                 : "memory");
+  } else {
+    r.a = static_cast<const float4 *>(p)[0];
+    r.b = static_cast<const float4 *>(p)[1];
+  }
 }
 
 // Per-channel fp32 parameters of this thread's channels (absent: `none`).
@@ -123,10 +148,11 @@ __device__ __forceinline__ float2 kept(const uint4 &bits, int e, uint32_t thr, f
 
 // ---- the ring ------------------------------------------------------------------
 // Rows come through a ring of D + 1 stages in shared memory, D rows ahead, by
-// 16-byte asynchronous copies (cp.async). Every thread copies exactly the
-// vectors that it reads back, so the ring needs no barrier, only the thread's
-// own wait for its copies; the bytes in flight no longer depend on how many
-// registers a warp's work takes.
+// 16-byte asynchronous copies (cp.async); the bytes in flight do not depend on
+// how many registers a warp's work takes. A bf16 vector is one copy, made by
+// the thread that reads it. An fp32 vector is two: the lanes that share a row
+// copy its pieces in order (each copy instruction whole sectors) and read their
+// own two afterwards, so the ring is shared by a warp and needs its barriers.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
@@ -136,35 +162,69 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Slot (stage, tensor, vector j) of this thread: 16-byte pieces of consecutive
-// threads are consecutive (no bank conflicts).
-template <typename T, int kThreads, int NT, int NV>
+template <typename T, int TPR, int NT, int NV, int kStages>
 struct Ring {
+  static constexpr int kThreads = TPR > 32 ? TPR : 256;
   static constexpr int kPieces = vec_bytes<T>() / 16;
   static constexpr int kStage = kThreads * NT * NV * vec_bytes<T>();
-  uint8_t *base;
-  uint32_t addr;
-  __device__ __forceinline__ void init(uint8_t *smem) {
-    base = smem + threadIdx.x * 16;
-    addr = static_cast<uint32_t>(__cvta_generic_to_shared(base));
-  }
-  static __device__ __forceinline__ int slot(int stage, int t, int j) {
-    return stage * kStage + (t * NV + j) * kPieces * kThreads * 16;
-  }
-  // a vector of a tensor (its first byte's place if it is not there: nothing is read, zeros arrive)
-  __device__ __forceinline__ void fetch(int stage, int t, int j, const void *tensor, int64_t vec, bool there) const {
-    const uint8_t *src = static_cast<const uint8_t *>(tensor) + (there ? vec * vec_bytes<T>() : 0);
+  static constexpr int W = TPR < 32 ? TPR : 32;  // lanes of a warp that share a row
+  uint8_t *base;     // this thread's vector of slot 0
+  uint32_t to[kPieces];  // and the pieces it copies, as shared addresses
+  bool ok[NV][kPieces];  // pieces inside the row
+  int lane_bytes;    // of a thread's first piece from its row's first byte
+
+  __device__ __forceinline__ void init(uint8_t *smem, int lane, int C8) {
+    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const int t = threadIdx.x, w = t & ~31, l = t & 31;  // 16-byte chunks of fp32: 64 a warp, 2 l and 2 l + 1 a lane
+    if constexpr (kPieces == 1) {
+      base = smem + t * 16;
+      to[0] = s + t * 16;
+      lane_bytes = lane * 16;
+    } else {
+      base = smem + (w * 2 + swizzle(2 * l)) * 16;
 #pragma unroll
-    for (int p = 0; p < kPieces; ++p) copy16(addr + slot(stage, t, j) + p * kThreads * 16, src + 16 * p, there);
+      for (int p = 0; p < kPieces; ++p) to[p] = s + (w * 2 + swizzle(l / W * 2 * W + p * W + l % W)) * 16;
+      lane_bytes = (lane / 32 * 64 + lane % 32) * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+        ok[j][p] = j * TPR + (kPieces == 1 ? lane : lane / 32 * 32 + (p * W + lane % 32) / 2) < C8;
+  }
+  // keeps eight lanes' 32-byte reads free of bank conflicts (chunk 2 l + 1 follows or precedes 2 l)
+  static __device__ __forceinline__ int swizzle(int chunk) { return chunk ^ ((chunk >> 3) & 1); }
+  static __device__ __forceinline__ int slot(int t, int j) { return (t * NV + j) * kPieces * kThreads * 16; }
+  // the stage after `stage` (stages are byte offsets)
+  static __device__ __forceinline__ int next(int stage) { return stage == (kStages - 1) * kStage ? 0 : stage + kStage; }
+  // a thread's pieces of vector j; `from`: byte of its first piece of the row's first vector (rows past the end: nothing
+  // is read, zeros arrive)
+  __device__ __forceinline__ void fetch(int stage, int t, int j, const void *tensor, int64_t from, bool row) const {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      const bool there = row && ok[j][p];
+      const int64_t at = there ? from + j * TPR * vec_bytes<T>() + p * W * 16 : 0;
+      copy16(to[p] + stage + slot(t, j), static_cast<const uint8_t *>(tensor) + at, there);
+    }
+  }
+  // before the slots of the stage read last are filled again
+  __device__ __forceinline__ void before_fetch() const {
+    if (kPieces > 1) __syncwarp();
+  }
+  // all but the newest N rows have arrived
+  template <int N>
+  __device__ __forceinline__ void arrived() const {
+    copies_wait<N>();
+    if (kPieces > 1) __syncwarp();
   }
   __device__ __forceinline__ void read(int stage, int t, int j, float2 (&f)[4]) const {
-    const uint8_t *p = base + slot(stage, t, j);
+    const uint8_t *p = base + stage + slot(t, j);
     Raw<T> r;
     if constexpr (kPieces == 1) {
       r.v = *reinterpret_cast<const uint4 *>(p);
     } else {
       r.a = *reinterpret_cast<const float4 *>(p);
-      r.b = *reinterpret_cast<const float4 *>(p + kThreads * 16);
+      r.b = *reinterpret_cast<const float4 *>(reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) ^ 16));
     }
     unpack(r, f);
   }
@@ -178,8 +238,10 @@ constexpr int block_of(int tpr) { return tpr > 32 ? tpr : 256; }
 // column sums, two parameters and four rows of 8 channels are 80 registers
 // before any address, so 512 threads with 128 registers; twice that for two
 // vectors.
-constexpr int blocks_per_sm(int tpr, int nv, bool bwd) {
-  return bwd ? (nv == 2 ? 1 : 512 / block_of(tpr)) : (nv == 2 ? 512 : 768) / block_of(tpr);
+constexpr int blocks_per_sm(int tpr, int nv, bool bwd, bool branch) {
+  return (bwd ? 512 / nv : nv == 2 ? 512 : branch ? 768 : 1024) / block_of(tpr) > 0
+             ? (bwd ? 512 / nv : nv == 2 ? 512 : branch ? 768 : 1024) / block_of(tpr)
+             : 1;
 }
 
 // Rows ahead: 64 KB in flight on an SM cover HBM's latency at its rate (about
@@ -194,7 +256,7 @@ constexpr int rows_ahead(int stage_bytes, int blocks) {
 template <typename T, int TPR, int NV, bool kBwd, bool kBranch, bool kPre>
 struct Shape {
   static constexpr int threads = block_of(TPR);
-  static constexpr int blocks = blocks_per_sm(TPR, NV, kBwd);
+  static constexpr int blocks = blocks_per_sm(TPR, NV, kBwd, kBranch);
   static constexpr int tensors = kBwd ? 1 + (kPre ? 2 : 0) + (kBranch ? 1 : 0) : (kBranch ? 2 : 1);
   static constexpr int stage = threads * tensors * NV * vec_bytes<T>();
   static constexpr int ahead = rows_ahead(stage, blocks);
@@ -204,17 +266,20 @@ struct Shape {
 };
 
 // ---- sums over a row ---------------------------------------------------------
-// Sums of a pair over the TPR threads of a row. Rows of up to 32 threads stay
-// inside a warp; wider rows are the whole CTA and exchange one pair per warp
-// through one of two shared buffers (used in turn: one barrier per sum).
-template <int TPR>
-__device__ __forceinline__ float2 row_sum(float2 v, float2 *xchg, int &turn) {
+// Sum of a float, or of a pair, over the TPR threads of a row. Rows of up to 32
+// threads stay inside a warp; wider rows are the whole CTA and exchange one
+// value per warp through one of two shared buffers (used in turn: one barrier
+// per sum).
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float shuffle_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ float2 shuffle_xor(float2 v, int o) { return make_float2(shuffle_xor(v.x, o), shuffle_xor(v.y, o)); }
+template <int TPR, typename V>
+__device__ __forceinline__ V row_sum(V v, float2 *xchg, int &turn) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
-    v = add(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v = add(v, shuffle_xor(v, o));
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
-    float2 *buf = xchg + turn * W;
+    V *buf = reinterpret_cast<V *>(xchg + turn * W);
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -254,35 +319,40 @@ __device__ __forceinline__ void centre(float2 (&u)[NV][4], float m, const bool (
   }
 }
 
-// Where a CTA's rows lie and which of them a thread works on.
+// Which of a CTA's rows a thread works on, and which channels.
 struct Place {
-  int lane, sub;
-  int64_t first, stride;
+  int lane, first, stride;  // thread of the row; its first row of the CTA's and the step to its next
 };
 template <int TPR>
 __device__ __forceinline__ Place place() {
   constexpr int kWarps = block_of(TPR) / 32, RPW = TPR < 32 ? 32 / TPR : 1;  // rows a warp works on at once
   Place p;
   p.lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
-  p.sub = TPR < 32 ? (threadIdx.x & 31) / TPR : 0;
-  p.first = TPR > 32 ? 0 : (threadIdx.x >> 5) * RPW;
+  p.first = TPR > 32 ? 0 : (threadIdx.x >> 5) * RPW + (TPR < 32 ? (threadIdx.x & 31) / TPR : 0);
   p.stride = TPR > 32 ? 1 : kWarps * RPW;
   return p;
+}
+// Trips a thread's warp makes over `count` rows (the same for its whole warp).
+template <int TPR>
+__device__ __forceinline__ int trips(const Place &p, int count) {
+  const int first = TPR < 32 ? p.first - (int)(threadIdx.x & 31) / TPR : p.first;
+  return first < count ? (count - first + p.stride - 1) / p.stride : 0;
 }
 
 // ---- forward -----------------------------------------------------------------
 template <typename T, int TPR, int NV, bool kBranch, bool kPre>
-__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false)) rows_fwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false, kBranch)) rows_fwd_kernel(const RowArgs a) {
   using S = Shape<T, TPR, NV, false, kBranch, kPre>;
-  constexpr int D = S::ahead;
-  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int D = S::ahead, VB = vec_bytes<T>();
+  using R = Ring<T, TPR, S::tensors, NV, D + 1>;
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
   int turn = 0;
   const Place pl = place<TPR>();
   const int C8 = a.C >> 3;
   const float inv = 1.0f / (float)a.C;
-  Ring<T, S::threads, S::tensors, NV> ring;
-  ring.init(smem);
+  R ring;
+  ring.init(smem, pl.lane, C8);
   bool ok[NV];
   float2 gpre[NV][4], bpre[NV][4], wg[NV][4], wb[NV][4];
 #pragma unroll
@@ -297,26 +367,29 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false)) 
   ph.init(a.drop);
   const bool post = a.post.kind != SWIN_NORM_NONE;
 
-  const int64_t L = (int64_t)blockIdx.x * a.chunk;
-  const int64_t R = min(L + a.chunk, a.rows);
+  const int64_t first = (int64_t)blockIdx.x * a.chunk, last = min(first + a.chunk, a.rows);
+  const int64_t step = (int64_t)pl.stride * C8;  // vectors from a thread's row to its next
   // one image of the CTA's rows at a time: the gate and the path decision change with it
-  for (int64_t s = L; s < R;) {
+  for (int64_t s = first; s < last;) {
     const int64_t b = s / a.tokens;
-    const int64_t e1 = min(R, (b + 1) * a.tokens);
-    auto fetch = [&](int64_t r0, int stage) {
-      const int64_t row = r0 + pl.sub, vec0 = row * C8 + pl.lane;
+    const int count = (int)(min(last, (b + 1) * a.tokens) - s), n = trips<TPR>(pl, count);
+    int64_t vec = (s + pl.first) * C8 + pl.lane;  // this row's first vector of the thread
+    int64_t to = vec * VB;                        // and its byte, `step` vectors a row
+    int64_t from = (s + pl.first) * C8 * VB + ring.lane_bytes;  // of its first piece of the row to fetch
+    int ahead = pl.first;
+    auto fetch = [&](int stage) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const bool there = ok[j] && row < e1;
-        ring.fetch(stage, 0, j, a.x, vec0 + j * TPR, there);
-        if constexpr (kBranch) ring.fetch(stage, 1, j, a.z, vec0 + j * TPR, there);
+        ring.fetch(stage, 0, j, a.x, from, ahead < count);
+        if constexpr (kBranch) ring.fetch(stage, 1, j, a.z, from, ahead < count);
       }
       copies_commit();
+      ahead += pl.stride;
+      from += step * VB;
     };
-    int64_t ahead = s + pl.first;
     int in = 0, out = 0;
 #pragma unroll
-    for (int k = 0; k < D; ++k, ahead += pl.stride) fetch(ahead, in++);
+    for (int k = 0; k < D; ++k, in += R::kStage) fetch(in);
     bool path = true;
     if constexpr (kBranch) {
       float c = a.drop.scale;  // what is kept is multiplied by, with the gate and the layer scale
@@ -341,13 +414,14 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false)) 
         for (int e = 0; e < 4; ++e) wb[j][e] = mul(wb[j][e], t[e]);
       }
     }
-    for (int64_t r0 = s + pl.first; r0 < e1; r0 += pl.stride, ahead += pl.stride) {
-      fetch(ahead, in);
-      in = in == D ? 0 : in + 1;
-      copies_wait<D>();
-      const int64_t row = r0 + pl.sub;
-      const bool live = row < e1;
-      const int64_t vec0 = row * C8 + pl.lane;
+    int row = pl.first;
+#pragma unroll 1
+    for (int k = 0; k < n; ++k, row += pl.stride, vec += step, to += step * VB) {
+      ring.before_fetch();
+      fetch(in);
+      in = R::next(in);
+      ring.template arrived<D>();
+      const bool live = row < count;
       float2 v[NV][4];
 #pragma unroll
       for (int j = 0; j < NV; ++j) ring.read(out, 0, j, v[j]);
@@ -355,48 +429,49 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false)) 
         float2 u[NV][4];
 #pragma unroll
         for (int j = 0; j < NV; ++j) ring.read(out, 1, j, u[j]);
-        float2 rstd = both(1.f);
         if (post) {
-          if (a.post.kind == SWIN_NORM_LAYER)
-            centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
-          rstd = both(rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.post.eps)));
+          if (a.post.kind == SWIN_NORM_LAYER) centre<NV>(u, row_sum<TPR>(sum_of<NV>(u), xchg, turn) * inv, ok);
+          const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(u, u), xchg, turn), inv, a.post.eps)));
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[j][e] = mul(u[j][e], rstd);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          if (path) {  // a dropped image's y is x
-            uint4 bits;
-            if (a.drop.thr) bits = ph.block((uint64_t)(vec0 + j * TPR));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 br = fma(mul(u[j][e], rstd), wg[j][e], wb[j][e]);
-              if (a.drop.thr) br = kept(bits, e, a.drop.thr, br);
-              v[j][e] = add(v[j][e], br);
-            }
+          for (int e = 0; e < 4; ++e) u[j][e] = fma(u[j][e], wg[j][e], wb[j][e]);
+          if (a.drop.thr) {
+            const uint4 bits = ph.block((uint64_t)(vec + j * TPR));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[j][e] = kept(bits, e, a.drop.thr, u[j][e]);
+          }
+          if (path) {  // a dropped image's y is x
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j][e] = add(v[j][e], u[j][e]);
           }
           Raw<T> o;
           pack(v[j], o);
-          if (ok[j] && live) store8(a.y, vec0 + j * TPR, o);
+          if (ok[j] && live) store8(a.y, to + j * TPR * VB, o, a.wide);
           if constexpr (kPre) unpack(o, v[j]);  // h is the norm of y as stored
         }
       }
-      out = out == D ? 0 : out + 1;
+      out = R::next(out);
       if constexpr (kPre) {
-        if (a.pre.kind == SWIN_NORM_LAYER)
-          centre<NV>(v, row_sum<TPR>(make_float2(sum_of<NV>(v), 0.f), xchg, turn).x * inv, ok);
-        const float2 rstd =
-            both(rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(v, v), 0.f), xchg, turn).x, inv, a.pre.eps)));
+        if (a.pre.kind == SWIN_NORM_LAYER) centre<NV>(v, row_sum<TPR>(sum_of<NV>(v), xchg, turn) * inv, ok);
+        const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(v, v), xchg, turn), inv, a.pre.eps)));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           Raw<T> o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[j][e] = fma(mul(v[j][e], rstd), gpre[j][e], bpre[j][e]);
           pack(v[j], o);
-          if (ok[j] && live) store8(a.h, vec0 + j * TPR, o);
+          if (ok[j] && live) store8(a.h, to + j * TPR * VB, o, a.wide);
         }
       }
     }
     copies_wait<0>();
-    s = e1;
+    s += count;
   }
 }
 
@@ -434,18 +509,19 @@ __device__ __forceinline__ void flush(float2 (&acc)[NV][4], float *dst, int C8, 
 }
 
 template <typename T, int TPR, int NV, bool kBranch, bool kPre>
-__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) rows_bwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kBranch)) rows_bwd_kernel(const RowArgs a) {
   using S = Shape<T, TPR, NV, true, kBranch, kPre>;
-  constexpr int D = S::ahead;
+  constexpr int D = S::ahead, VB = vec_bytes<T>();
+  using R = Ring<T, TPR, S::tensors, NV, D + 1>;
   constexpr int tDy = 0, tY = 1, tDh = 2, tZ = kPre ? 3 : 1;  // tensors of a stage
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
   int turn = 0;
   const Place pl = place<TPR>();
   const int C8 = a.C >> 3;
   const float inv = 1.0f / (float)a.C;
-  Ring<T, S::threads, S::tensors, NV> ring;
-  ring.init(smem);
+  R ring;
+  ring.init(smem, pl.lane, C8);
   bool ok[NV];
   float2 gpre[NV][4], w[NV][4];
   float2 a1[NV][4], a0[NV][4], b1[NV][4], b0[NV][4];  // column sums: dh yhat, dh; G zhat, G
@@ -458,32 +534,35 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) r
   }
   Philox ph;
   ph.init(a.drop);
-  const bool post = a.post.kind != SWIN_NORM_NONE;
+  const bool post = kBranch && a.post.kind != SWIN_NORM_NONE;
+  const bool post_layer = kBranch && a.post.kind == SWIN_NORM_LAYER, pre_layer = kPre && a.pre.kind == SWIN_NORM_LAYER;
 
-  const int64_t L = (int64_t)blockIdx.x * a.chunk;
-  const int64_t R = min(L + a.chunk, a.rows);
-  for (int64_t s = L; s < R;) {
+  const int64_t first = (int64_t)blockIdx.x * a.chunk, last = min(first + a.chunk, a.rows);
+  const int64_t step = (int64_t)pl.stride * C8;
+  for (int64_t s = first; s < last;) {
     const int64_t b = s / a.tokens;
-    const int64_t e1 = min(R, (b + 1) * a.tokens);
-    auto fetch = [&](int64_t r0, int stage) {
-      const int64_t row = r0 + pl.sub, vec0 = row * C8 + pl.lane;
+    const int count = (int)(min(last, (b + 1) * a.tokens) - s), n = trips<TPR>(pl, count);
+    int64_t vec = (s + pl.first) * C8 + pl.lane;
+    int64_t to = vec * VB, from = (s + pl.first) * C8 * VB + ring.lane_bytes;
+    int ahead = pl.first;
+    auto fetch = [&](int stage) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const bool there = ok[j] && row < e1;
-        if (a.dy) ring.fetch(stage, tDy, j, a.dy, vec0 + j * TPR, there);
+        if (a.dy) ring.fetch(stage, tDy, j, a.dy, from, ahead < count);
         if constexpr (kPre) {
-          ring.fetch(stage, tY, j, a.x, vec0 + j * TPR, there);
-          ring.fetch(stage, tDh, j, a.dh, vec0 + j * TPR, there);
+          ring.fetch(stage, tY, j, a.x, from, ahead < count);
+          ring.fetch(stage, tDh, j, a.dh, from, ahead < count);
         }
         if constexpr (kBranch)
-          if (a.z) ring.fetch(stage, tZ, j, a.z, vec0 + j * TPR, there);
+          if (a.z) ring.fetch(stage, tZ, j, a.z, from, ahead < count);
       }
       copies_commit();
+      ahead += pl.stride;
+      from += step * VB;
     };
-    int64_t ahead = s + pl.first;
     int in = 0, out = 0;
 #pragma unroll
-    for (int k = 0; k < D; ++k, ahead += pl.stride) fetch(ahead, in++);
+    for (int k = 0; k < D; ++k, in += R::kStage) fetch(in);
     bool path = true;
     if constexpr (kBranch) {
       float c = a.drop.scale;  // the kept values' scales: in dz here, in the column sums at the fold
@@ -505,13 +584,56 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) r
         for (int e = 0; e < 4; ++e) w[j][e] = mul(w[j][e], t[e]);
       }
     }
-    for (int64_t r0 = s + pl.first; r0 < e1; r0 += pl.stride, ahead += pl.stride) {
-      fetch(ahead, in);
-      in = in == D ? 0 : in + 1;
-      copies_wait<D>();
-      const int64_t row = r0 + pl.sub;
-      const bool live = row < e1;  // rows past the end arrived as zeros and add nothing to the sums
-      const int64_t vec0 = row * C8 + pl.lane;
+    int row = pl.first;
+    // Vectors past a row's end and rows past the last arrive as zeros and stay
+    // zeros (u, dh, g), so they add nothing to any sum.
+#pragma unroll 1
+    for (int k = 0; k < n; ++k, row += pl.stride, vec += step, to += step * VB) {
+      ring.before_fetch();
+      fetch(in);
+      in = R::next(in);
+      ring.template arrived<D>();
+      const bool live = row < count;
+      // both rows' statistics, in two rounds of sums
+      float2 y[NV][4], z[NV][4];
+      float y_rstd = 1.f, z_rstd = 1.f;
+      if constexpr (kPre) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) ring.read(out, tY, j, y[j]);
+      }
+      if constexpr (kBranch) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          if (a.z && path) {
+            ring.read(out, tZ, j, z[j]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[j][e] = make_float2(0.f, 0.f);
+          }
+        }
+      }
+      if constexpr (kPre && kBranch) {
+        if (post) {
+          if (pre_layer || post_layer) {
+            const float2 m = row_sum<TPR>(make_float2(sum_of<NV>(y), sum_of<NV>(z)), xchg, turn);
+            if (pre_layer) centre<NV>(y, m.x * inv, ok);
+            if (post_layer) centre<NV>(z, m.y * inv, ok);
+          }
+          const float2 q = row_sum<TPR>(make_float2(dot_of<NV>(y, y), dot_of<NV>(z, z)), xchg, turn);
+          y_rstd = rsqrtf(fmaf(q.x, inv, a.pre.eps));
+          z_rstd = rsqrtf(fmaf(q.y, inv, a.post.eps));
+        }
+      }
+      if constexpr (kPre)
+        if (!kBranch || !post) {
+          if (pre_layer) centre<NV>(y, row_sum<TPR>(sum_of<NV>(y), xchg, turn) * inv, ok);
+          y_rstd = rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(y, y), xchg, turn), inv, a.pre.eps));
+        }
+      if constexpr (kBranch && !kPre)
+        if (post) {
+          if (post_layer) centre<NV>(z, row_sum<TPR>(sum_of<NV>(z), xchg, turn) * inv, ok);
+          z_rstd = rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(z, z), xchg, turn), inv, a.post.eps));
+        }
       float2 g[NV][4];  // dy, then dy' = dx
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -523,100 +645,104 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) r
         }
       }
       if constexpr (kPre) {
-        float2 u[NV][4], dh[NV][4];
+        float2 dh[NV][4];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          ring.read(out, tY, j, u[j]);
           ring.read(out, tDh, j, dh[j]);
-        }
-        const bool layer = a.pre.kind == SWIN_NORM_LAYER;
-        if (layer) centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
-        const float rstd = rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.pre.eps));
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            u[j][e] = mul(u[j][e], both(rstd));
-            a1[j][e] = fma(dh[j][e], u[j][e], a1[j][e]);
+            y[j][e] = mul(y[j][e], both(y_rstd));
+            a1[j][e] = fma(dh[j][e], y[j][e], a1[j][e]);
             a0[j][e] = add(a0[j][e], dh[j][e]);
             dh[j][e] = mul(dh[j][e], gpre[j][e]);
           }
-        const float2 c = row_sum<TPR>(make_float2(dot_of<NV>(dh, u), layer ? sum_of<NV>(dh) : 0.f), xchg, turn);
-        const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
+        }
+        float2 c = make_float2(dot_of<NV>(dh, y), 0.f);
+        if (pre_layer) {
+          c.y = sum_of<NV>(dh);
+          c = row_sum<TPR>(c, xchg, turn);
+        } else {
+          c.x = row_sum<TPR>(c.x, xchg, turn);
+        }
+        const float2 c1 = both(-c.x * inv);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j) {
+          const float2 c0 = both(ok[j] ? -c.y * inv : 0.f);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            g[j][e] = fma(both(rstd), add(dh[j][e], fma(u[j][e], c1, c0)), g[j][e]);
+            g[j][e] = fma(both(y_rstd), add(dh[j][e], fma(y[j][e], c1, c0)), g[j][e]);
+        }
       }
+      out = R::next(out);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         Raw<T> o;
         pack(g[j], o);
-        if (ok[j] && live) store8(a.dx, vec0 + j * TPR, o);
+        if (ok[j] && live) store8(a.dx, to + j * TPR * VB, o, a.wide);
       }
       if constexpr (kBranch) {
-        float2 u[NV][4];
+        if (path) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          if (a.z && path) {
-            ring.read(out, tZ, j, u[j]);
-          } else {
+          for (int j = 0; j < NV; ++j) {
+            if (post) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) u[j][e] = make_float2(0.f, 0.f);
-          }
-        }
-        const bool layer = a.post.kind == SWIN_NORM_LAYER;
-        float rstd = 1.f;
-        if (layer) centre<NV>(u, row_sum<TPR>(make_float2(sum_of<NV>(u), 0.f), xchg, turn).x * inv, ok);
-        if (post) rstd = rsqrtf(fmaf(row_sum<TPR>(make_float2(dot_of<NV>(u, u), 0.f), xchg, turn).x, inv, a.post.eps));
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const bool in_row = ok[j] && live;  // past the row's end dy' is not 0
-          uint4 bits;
-          if (a.drop.thr) bits = ph.block((uint64_t)(vec0 + j * TPR));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            u[j][e] = mul(u[j][e], both(rstd));
-            if (!path || !in_row) g[j][e] = make_float2(0.f, 0.f);
-            if (a.drop.thr) {
-              g[j][e] = kept(bits, e, a.drop.thr, g[j][e]);
-              // what was dropped takes no part, were it infinite (a row's norm has it in its statistics anyway)
-              if (!post) u[j][e] = kept(bits, e, a.drop.thr, u[j][e]);
+              for (int e = 0; e < 4; ++e) z[j][e] = mul(z[j][e], both(z_rstd));
             }
-            b1[j][e] = fma(g[j][e], u[j][e], b1[j][e]);
-            b0[j][e] = add(b0[j][e], g[j][e]);
-            g[j][e] = mul(g[j][e], w[j][e]);
+            if (a.drop.thr) {
+              const uint4 bits = ph.block((uint64_t)(vec + j * TPR));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                g[j][e] = kept(bits, e, a.drop.thr, g[j][e]);
+                // what was dropped takes no part, were it infinite (a row's norm has it in its statistics anyway)
+                if (!post) z[j][e] = kept(bits, e, a.drop.thr, z[j][e]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              b1[j][e] = fma(g[j][e], z[j][e], b1[j][e]);
+              b0[j][e] = add(b0[j][e], g[j][e]);
+              g[j][e] = mul(g[j][e], w[j][e]);
+            }
           }
-        }
-        if (post) {
-          const float2 c = row_sum<TPR>(make_float2(dot_of<NV>(g, u), layer ? sum_of<NV>(g) : 0.f), xchg, turn);
-          const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
+          if (post) {
+            float2 c = make_float2(dot_of<NV>(g, z), 0.f);
+            if (post_layer) {
+              c.y = sum_of<NV>(g);
+              c = row_sum<TPR>(c, xchg, turn);
+            } else {
+              c.x = row_sum<TPR>(c.x, xchg, turn);
+            }
+            const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) g[j][e] = mul(both(z_rstd), add(g[j][e], fma(z[j][e], c1, c0)));
+          }
+        } else {  // a dropped image: no gradient reaches z
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) g[j][e] = mul(both(rstd), add(g[j][e], fma(u[j][e], c1, c0)));
+            for (int e = 0; e < 4; ++e) g[j][e] = make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           Raw<T> o;
           pack(g[j], o);
-          if (ok[j] && live) store8(a.dz, vec0 + j * TPR, o);
+          if (ok[j] && live) store8(a.dz, to + j * TPR * VB, o, a.wide);
         }
       }
-      out = out == D ? 0 : out + 1;
     }
     copies_wait<0>();
+    s += count;
     // with a gate the sums are kept per image: slot CTA + image (a CTA's next
     // image takes its next slot, the next CTA's first is one further)
     if constexpr (kBranch)
-      if (a.part_post && (a.gate || e1 == R)) {
+      if (a.part_post && (a.gate || s == last)) {
         float *dst = a.part_post + ((int64_t)blockIdx.x + (a.gate ? b : 0)) * 2 * a.C;
         flush<TPR, NV>(b1, dst, C8, reinterpret_cast<float *>(smem));
         flush<TPR, NV>(b0, dst + a.C, C8, reinterpret_cast<float *>(smem));
         if (TPR <= 32) __syncthreads();  // the ring takes the buffer again
       }
-    s = e1;
   }
   if constexpr (kPre)
     if (a.part_pre) {
@@ -628,100 +754,99 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true)) r
 
 // ---- parameter gradients from the column sums ----------------------------------
 struct ColArgs {
-  int64_t tokens, chunk, rows;
-  int images, C, ctas;
+  int64_t tokens, chunk;
+  int images, C, ctas;  // ctas: slots of each CTA sum (0: no rows)
   bool post_norm;
   float kept;  // what kept values are multiplied by (left out of the join's sums)
   const float *part_pre, *part_post;
   const float *scale, *gate, *gamma, *beta;  // gamma, beta: the post norm's
   float *dpre_gamma, *dpre_beta, *dpost_gamma, *dpost_beta, *dscale, *dgate;
+  float *groups;  // [gridDim.y][2][C] gate-weighted sums of each group of images, where there are several
 };
 
-constexpr int kColLanes = 16;
+constexpr int kColLanes = 32, kGroupImages = 256, kFewImages = 8;
 
-// Sum over the lanes of a block (32 channels x kColLanes), in lane order.
-__device__ __forceinline__ float lane_sum(float v, float *buf) {
+struct Sums {
+  float one, zero;  // of the terms with xhat, and of those without
+};
+
+// Adds up the lanes of a block (32 channels x kColLanes) in a fixed order: warp y
+// sums channel y, so thread (0, y) has the result.
+__device__ __forceinline__ Sums lane_sum(Sums v, float2 (&buf)[kColLanes][33]) {
   __syncthreads();
-  buf[threadIdx.y * 32 + threadIdx.x] = v;
+  buf[threadIdx.y][threadIdx.x] = make_float2(v.one, v.zero);
   __syncthreads();
-  float s = 0.f;
-  if (threadIdx.y == 0)
+  float2 s = buf[threadIdx.x][threadIdx.y];
 #pragma unroll
-    for (int k = 0; k < kColLanes; ++k) s += buf[k * 32 + threadIdx.x];
-  return s;
+  for (int o = 16; o > 0; o >>= 1) s = add(s, shuffle_xor(s, o));
+  return {s.x, s.y};
 }
 
-// Block (tile, 0): the sums over all rows of 32 channels. Block (tile, 1 + b):
-// image b's gate gradient.
+// Slots s0 ... s1 of channel c, every `step`th.
+__device__ __forceinline__ Sums slot_sum(const float *part, int s0, int s1, int step, int C, int c) {
+  Sums v = {0.f, 0.f};
+  const float *p = part + (int64_t)s0 * 2 * C + c;
+#pragma unroll 8
+  for (int s = s0; s <= s1; s += step, p += (int64_t)step * 2 * C) {
+    v.one += p[0];
+    v.zero += p[C];
+  }
+  return v;
+}
+
+// Block (tile, group, 0 or 1): 32 channels. z = 0: the pre norm's sums over all
+// rows. z = 1: the join's, and with a gate each group its images: their gate
+// gradients and their gate-weighted sum. The pair (CTA r, image b) has slot
+// r + b, so image b owns the slots from its first row's CTA to its last row's.
+// A few images share the lanes; many take a lane each.
 __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a) {
-  __shared__ float buf[32 * kColLanes];
-  const int tiles = (a.C + 31) / 32;
-  const int tile = (int)(blockIdx.x % tiles);
-  const int64_t task = blockIdx.x / tiles;
-  const int c = tile * 32 + threadIdx.x, cc = min(c, a.C - 1);
-  const bool own = threadIdx.y == 0 && c < a.C;
-  const int64_t C2 = 2 * (int64_t)a.C;
-  if (task > 0) {
-    const int64_t b = task - 1;
-    const int64_t s0 = a.tokens * b / a.chunk + b, s1 = (a.tokens * (b + 1) - 1) / a.chunk + b;
-    float v1 = 0.f, v0 = 0.f;
-    if (a.rows)
-      for (int64_t s = s0 + threadIdx.y; s <= s1; s += kColLanes) {
-        v1 += a.part_post[s * C2 + cc];
-        v0 += a.part_post[s * C2 + a.C + cc];
-      }
-    v1 = a.kept * lane_sum(v1, buf);
-    v0 = a.kept * lane_sum(v0, buf);
-    if (own) {
-      const float gm = a.post_norm && a.gamma ? a.gamma[c] : 1.f, bt = a.post_norm && a.beta ? a.beta[c] : 0.f;
-      a.dgate[b * a.C + c] = (a.scale ? a.scale[c] : 1.f) * fmaf(gm, v1, bt * v0);
-    }
+  static_assert(kColLanes == 32, "a warp sums the lanes of a channel");
+  __shared__ float2 buf[kColLanes][33];
+  const int tile = blockIdx.x * 32, lane = threadIdx.y;
+  const int cc = min(tile + (int)threadIdx.x, a.C - 1);  // the channel this thread sums
+  const int c = tile + (int)threadIdx.y;                 // the channel whose result its warp gets
+  const bool own = threadIdx.x == 0 && c < a.C;
+  if (blockIdx.z == 0) {
+    if (blockIdx.y > 0 || !(a.dpre_gamma || a.dpre_beta)) return;
+    const Sums v = lane_sum(slot_sum(a.part_pre, lane, a.ctas - 1, kColLanes, a.C, cc), buf);
+    if (own && a.dpre_gamma) a.dpre_gamma[c] = v.one;
+    if (own && a.dpre_beta) a.dpre_beta[c] = v.zero;
     return;
   }
-  if (a.dpre_gamma || a.dpre_beta) {
-    float v1 = 0.f, v0 = 0.f;
-#pragma unroll 4
-    for (int s = threadIdx.y; s < a.ctas; s += kColLanes) {
-      v1 += a.part_pre[s * C2 + cc];
-      v0 += a.part_pre[s * C2 + a.C + cc];
+  if (!a.dpost_gamma && !a.dpost_beta && !a.dscale && !a.dgate) return;
+  auto at = [&](const float *p, int ch, float none) { return p ? p[min(ch, a.C - 1)] : none; };
+  const float *gamma = a.post_norm ? a.gamma : nullptr, *beta = a.post_norm ? a.beta : nullptr;
+  Sums all = {0.f, 0.f};
+  if (!a.gate) {
+    all = lane_sum(slot_sum(a.part_post, lane, a.ctas - 1, kColLanes, a.C, cc), buf);
+  } else {
+    const int tokens = (int)a.tokens, chunk = (int)a.chunk;  // both, and all rows, below 2^31
+    const int b0 = blockIdx.y * kGroupImages, b1 = min(b0 + kGroupImages, a.images);
+    const bool few = b1 - b0 <= kFewImages;
+    for (int b = few ? b0 : b0 + lane; b < b1; b += few ? 1 : kColLanes) {
+      const int s0 = tokens * b / chunk + b, s1 = a.ctas ? (tokens * (b + 1) - 1) / chunk + b : s0 - 1;
+      Sums v = slot_sum(a.part_post, s0 + (few ? lane : 0), s1, few ? kColLanes : 1, a.C, cc);
+      if (few) v = lane_sum(v, buf);
+      const int ch = few ? c : tile + (int)threadIdx.x;
+      if (ch < a.C) {
+        const float g = a.gate[(int64_t)b * a.C + ch];
+        all.one = fmaf(g, v.one, all.one);
+        all.zero = fmaf(g, v.zero, all.zero);
+        if (a.dgate && (!few || threadIdx.x == 0))
+          a.dgate[(int64_t)b * a.C + ch] =
+              a.kept * at(a.scale, ch, 1.f) * fmaf(at(gamma, ch, 1.f), v.one, at(beta, ch, 0.f) * v.zero);
+      }
     }
-    v1 = lane_sum(v1, buf);
-    v0 = lane_sum(v0, buf);
-    if (own && a.dpre_gamma) a.dpre_gamma[c] = v1;
-    if (own && a.dpre_beta) a.dpre_beta[c] = v0;
+    if (!few) all = lane_sum(all, buf);
   }
-  if (a.dpost_gamma || a.dpost_beta || a.dscale) {
-    float v1 = 0.f, v0 = 0.f;
-    if (a.gate) {
-      // slot s of the pair (CTA r, image b) is r + b; image b owns the slots
-      // from its first row's CTA to its last row's
-      const int64_t slots = a.rows ? a.ctas + a.images - 1 : 0;
-      const double per = (double)a.chunk / ((double)a.chunk + (double)a.tokens);
-      for (int64_t s = threadIdx.y; s < slots; s += kColLanes) {
-        int64_t b = min((int64_t)(s * per), (int64_t)a.images - 1);
-        while (b > 0 && a.tokens * b / a.chunk + b > s) --b;
-        while (b + 1 < a.images && a.tokens * (b + 1) / a.chunk + (b + 1) <= s) ++b;
-        if ((a.tokens * (b + 1) - 1) / a.chunk + b < s) continue;  // an image ended with its CTA: slot not used
-        const float gt = a.gate[b * a.C + cc];
-        v1 = fmaf(gt, a.part_post[s * C2 + cc], v1);
-        v0 = fmaf(gt, a.part_post[s * C2 + a.C + cc], v0);
-      }
-    } else {
-#pragma unroll 4
-      for (int s = threadIdx.y; s < a.ctas; s += kColLanes) {
-        v1 += a.part_post[s * C2 + cc];
-        v0 += a.part_post[s * C2 + a.C + cc];
-      }
-    }
-    v1 = a.kept * lane_sum(v1, buf);
-    v0 = a.kept * lane_sum(v0, buf);
-    if (own) {
-      const float sc = a.scale ? a.scale[c] : 1.f;
-      const float gm = a.post_norm && a.gamma ? a.gamma[c] : 1.f, bt = a.post_norm && a.beta ? a.beta[c] : 0.f;
-      if (a.dpost_gamma) a.dpost_gamma[c] = sc * v1;
-      if (a.dpost_beta) a.dpost_beta[c] = sc * v0;
-      if (a.dscale) a.dscale[c] = fmaf(gm, v1, bt * v0);
-    }
+  if (!own) return;
+  if (a.groups) {
+    a.groups[(int64_t)blockIdx.y * 2 * a.C + c] = all.one;
+    a.groups[(int64_t)blockIdx.y * 2 * a.C + a.C + c] = all.zero;
+  } else {
+    if (a.dpost_gamma) a.dpost_gamma[c] = a.kept * at(a.scale, c, 1.f) * all.one;
+    if (a.dpost_beta) a.dpost_beta[c] = a.kept * at(a.scale, c, 1.f) * all.zero;
+    if (a.dscale) a.dscale[c] = a.kept * fmaf(at(gamma, c, 1.f), all.one, at(beta, c, 0.f) * all.zero);
   }
 }
 
@@ -730,7 +855,7 @@ __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a
 // 8-element vector; 1: span a multiple of 8, one decision per vector; 2: any
 // other span, one decision per element.
 template <typename T, int kMode>
-__global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t n, int64_t span, Drop d) {
+__global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t n, int64_t span, Drop d, bool wide) {
   Philox ph;
   ph.init(d);
   const int64_t nvec = (n + 7) >> 3;
@@ -740,7 +865,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
     if (kMode == 0) bits = ph.block((uint64_t)v);
     if (kMode == 1 && keep_one(ph, (uint64_t)(i0 / span), d.thr)) bits = make_uint4(~0u, ~0u, ~0u, ~0u);
     if (i0 + 8 <= n) {
-      const Raw<T> in = *reinterpret_cast<const Raw<T> *>(x + i0);
+      Raw<T> in;
+      load8(x + i0, in, wide);
       float2 f[4];
       unpack(in, f);
 #pragma unroll
@@ -755,7 +881,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
       }
       Raw<T> out;
       pack(f, out);
-      store8(y, v, out);
+      store8(y, i0 * (int64_t)sizeof(T), out, wide);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -792,11 +918,11 @@ struct Split {
 };
 
 // Consecutive rows per CTA, as many CTAs as fit on the GPU at once.
-Split split_rows(int64_t rows, int C, int sms, bool bwd) {
+Split split_rows(int64_t rows, int C, int sms, bool bwd, bool branch) {
   const Width wd = width_of(C);
   const int64_t at_once = wd.tpr > 32 ? 1 : 256 / wd.tpr;
   const int64_t groups = (rows + at_once - 1) / at_once;
-  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)sms * blocks_per_sm(wd.tpr, wd.nv, bwd)));
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)sms * blocks_per_sm(wd.tpr, wd.nv, bwd, branch)));
   int64_t chunk = (rows + ctas - 1) / ctas;
   chunk = std::max<int64_t>(1, (chunk + at_once - 1) / at_once * at_once);
   return {chunk, (int)((rows + chunk - 1) / chunk)};
@@ -881,7 +1007,9 @@ bool overlap(const void *p, const void *q, size_t bytes) {
   return p && q && a < b + bytes && b < a + bytes;
 }
 
-int64_t col_slots(int ctas, int64_t images) { return (int64_t)ctas + std::max<int64_t>(images, 1); }
+// Column sums in the workspace: of the pre norm [ctas], of the join [ctas + images], of image groups.
+int64_t join_slots(int ctas, int64_t images) { return (int64_t)ctas + std::max<int64_t>(images, 1); }
+int64_t image_groups(int64_t images) { return std::max<int64_t>(1, (images + kGroupImages - 1) / kGroupImages); }
 
 }  // namespace
 }  // namespace swin
@@ -895,8 +1023,9 @@ size_t swin_attn_rows_workspace_bytes(const swin_attn_rows *r) {
   size_t bytes = 0;
   int sms = 0;
   if (check_rows(r, &rows, &bytes) || sm_count(&sms)) return 0;
-  const Split sp = split_rows(rows, r->channels, sms, true);
-  const size_t need = ((size_t)sp.ctas + (size_t)col_slots(sp.ctas, r->images)) * 2 * r->channels * sizeof(float);
+  const Split sp = split_rows(rows, r->channels, sms, true, true);
+  const size_t slots = (size_t)(sp.ctas + join_slots(sp.ctas, r->images) + image_groups(r->images));
+  const size_t need = slots * 2 * r->channels * sizeof(float);
   return (need + 255) & ~size_t(255);
 }
 
@@ -917,11 +1046,12 @@ int swin_attn_norm_fwd(const swin_attn_rows *r, const void *x, const swin_attn_n
   if (rc) return rc;
   a.x = x;
   a.h = h;
+  a.wide = !mis(h, 32);
   a.tokens = a.rows;
   a.images = 1;
   a.C = r->channels;
   a.path.scale = a.drop.scale = 1.f;
-  const Split sp = split_rows(a.rows, a.C, sms, false);
+  const Split sp = split_rows(a.rows, a.C, sms, false, false);
   a.chunk = sp.chunk;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return r->dtype == SWIN_BF16 ? launch_width<__nv_bfloat16>(a, false, false, true, sp.ctas, st)
@@ -953,12 +1083,13 @@ int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, co
   a.z = z;
   a.y = y;
   a.h = h;
+  a.wide = !mis(y, 32) && !mis(h, 32);
   a.scale = join->scale;
   a.gate = join->gate;
   a.tokens = r->tokens;
   a.images = (int)r->images;
   a.C = r->channels;
-  const Split sp = split_rows(a.rows, a.C, sms, false);
+  const Split sp = split_rows(a.rows, a.C, sms, false, true);
   a.chunk = sp.chunk;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return r->dtype == SWIN_BF16 ? launch_width<__nv_bfloat16>(a, false, true, pre, sp.ctas, st)
@@ -981,7 +1112,7 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   a.C = r->channels;
   a.images = (int)r->images;
   a.tokens = branch ? r->tokens : a.rows;  // the norm alone does not look at images
-  const Split sp = split_rows(a.rows, a.C, sms, true);
+  const Split sp = split_rows(a.rows, a.C, sms, true, true);
   a.chunk = sp.chunk;
   if (want_pre || want_post) {
     if (!workspace || workspace_bytes < swin_attn_rows_workspace_bytes(r)) return SWIN_ERR_WORKSPACE;
@@ -997,7 +1128,6 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   }
   if (!want_pre && !want_post) return SWIN_OK;
   ColArgs c = {};
-  c.rows = a.rows;
   c.tokens = a.tokens;
   c.chunk = a.chunk;
   c.images = a.images;
@@ -1021,10 +1151,18 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
     c.dscale = g.scale;
     c.dgate = g.gate;
   }
-  const int64_t tiles = (a.C + 31) / 32;
-  const int64_t blocks = tiles * (1 + (c.dgate ? (int64_t)a.images : 0));
-  if (blocks > INT32_MAX) return SWIN_ERR_UNSUPPORTED;
-  columns_kernel<<<(int)blocks, dim3(32, kColLanes), 0, st>>>(c);
+  const int tiles = (a.C + 31) / 32;
+  const int64_t groups = a.gate && want_post ? image_groups(a.images) : 1;
+  if (groups > 65535) return SWIN_ERR_UNSUPPORTED;
+  if (groups > 1) c.groups = a.part_post + join_slots(sp.ctas, a.images) * 2 * a.C;
+  columns_kernel<<<dim3(tiles, (unsigned)groups, 2), dim3(32, kColLanes), 0, st>>>(c);
+  if (groups > 1) {  // the groups' sums are what a join without a gate would have left
+    c.part_post = c.groups;
+    c.ctas = (int)groups;
+    c.gate = nullptr;
+    c.groups = c.dgate = c.dpre_gamma = c.dpre_beta = nullptr;
+    columns_kernel<<<dim3(tiles, 1, 2), dim3(32, kColLanes), 0, st>>>(c);
+  }
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }
 
@@ -1052,6 +1190,7 @@ int swin_attn_norm_bwd(const swin_attn_rows *r, const void *x, const swin_attn_n
   a.dh = dh;
   a.dy = dres;
   a.dx = dx;
+  a.wide = !mis(dx, 32);
   a.path.scale = a.drop.scale = 1.f;
   swin_attn_join_grads g = {};
   g.pre_gamma = dgamma;
@@ -1096,6 +1235,7 @@ int swin_attn_join_bwd(const swin_attn_rows *r, const void *y, const void *z, co
   a.dh = dh;
   a.dx = dx;
   a.dz = dz;
+  a.wide = !mis(dx, 32) && !mis(dz, 32);
   a.scale = join->scale;
   a.gate = join->gate;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1132,15 +1272,15 @@ int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, con
   if (dtype == SWIN_BF16) {
     const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(x);
     __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(y);
-    if (mode == 0) dropout_kernel<__nv_bfloat16, 0><<<blocks, 256, 0, st>>>(p, q, n, span, d);
-    else if (mode == 1) dropout_kernel<__nv_bfloat16, 1><<<blocks, 256, 0, st>>>(p, q, n, span, d);
-    else dropout_kernel<__nv_bfloat16, 2><<<blocks, 256, 0, st>>>(p, q, n, span, d);
+    if (mode == 0) dropout_kernel<__nv_bfloat16, 0><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
+    else if (mode == 1) dropout_kernel<__nv_bfloat16, 1><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
+    else dropout_kernel<__nv_bfloat16, 2><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
   } else {
     const float *p = static_cast<const float *>(x);
     float *q = static_cast<float *>(y);
-    if (mode == 0) dropout_kernel<float, 0><<<blocks, 256, 0, st>>>(p, q, n, span, d);
-    else if (mode == 1) dropout_kernel<float, 1><<<blocks, 256, 0, st>>>(p, q, n, span, d);
-    else dropout_kernel<float, 2><<<blocks, 256, 0, st>>>(p, q, n, span, d);
+    if (mode == 0) dropout_kernel<float, 0><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
+    else if (mode == 1) dropout_kernel<float, 1><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
+    else dropout_kernel<float, 2><<<blocks, 256, 0, st>>>(p, q, n, span, d, !mis(x, 32) && !mis(y, 32));
   }
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }

@@ -248,6 +248,30 @@ def test_in_place_and_same_bits_again():
     assert torch.equal(apply_dropout(x4, drop, out=x4), apply_dropout(x, drop))
 
 
+def test_tensors_on_16_byte_boundaries():
+    """The contract asks for 16 bytes: fp32 tensors 16 off a 32-byte boundary give the same bits as aligned ones."""
+    from shifted_window_attention_cyclic_gb300.dropout import apply_dropout
+    from shifted_window_attention_cyclic_gb300.residual import BlockNorm, ResidualJoin
+    for c in (40, 256, 1032):
+        case, par, _, drop, path, _, _ = join_case(c, 2, 77, c, "f32", "layer", "rms", ALL, 0.2, 0.3)
+        x, z, dy, dh = (case[n][0] for n in ("x", "z", "dy", "dh"))
+
+        def off(t):
+            flat = torch.empty(t.numel() + 4, device="cuda", dtype=t.dtype)[4:].view(t.shape)
+            assert flat.data_ptr() % 32 == 16
+            return flat.copy_(t)
+
+        join, norm = ResidualJoin(c, "layer", "rms", dtype="f32"), BlockNorm(c, dtype="f32")
+        y, h = join.forward(x, z, **par, drop=drop, path=path)
+        y2, h2 = join.forward(off(x), off(z), **par, drop=drop, path=path, y=off(x), h=off(x))
+        assert torch.equal(y, y2) and torch.equal(h, h2)
+        a, b = (join.backward(f(y), f(z), f(dy), f(dh), **par, drop=drop, path=path) for f in (lambda t: t, off))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        assert torch.equal(norm.forward(x), norm.forward(off(x), h=off(x)))
+        assert torch.equal(norm.backward(x, dy)[0], norm.backward(off(x), off(dy), dx=off(x))[0])
+        assert torch.equal(apply_dropout(x, drop), apply_dropout(off(x), drop, out=off(x)))
+
+
 def test_other_stream_and_captured():
     """A backward on a side stream while another runs on the current one, and a
     captured step whose replays take the state's step."""
