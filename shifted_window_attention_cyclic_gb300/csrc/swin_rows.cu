@@ -744,6 +744,7 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
         if (TPR <= 32) __syncthreads();  // the ring takes the buffer again
       }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if constexpr (kPre)
     if (a.part_pre) {
       float *dst = a.part_pre + (int64_t)blockIdx.x * 2 * a.C;
@@ -764,7 +765,7 @@ struct ColArgs {
   float *groups;  // [gridDim.y][2][C] gate-weighted sums of each group of images, where there are several
 };
 
-constexpr int kColLanes = 32, kGroupImages = 256, kFewImages = 8;
+constexpr int kColLanes = 32, kGroupImages = 256, kFewImages = 4;
 
 struct Sums {
   float one, zero;  // of the terms with xhat, and of those without
@@ -801,6 +802,8 @@ __device__ __forceinline__ Sums slot_sum(const float *part, int s0, int s1, int 
 // A few images share the lanes; many take a lane each.
 __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a) {
   static_assert(kColLanes == 32, "a warp sums the lanes of a channel");
+  // launched while the row kernel's last CTAs still run: their sums are there after this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float2 buf[kColLanes][33];
   const int tile = blockIdx.x * 32, lane = threadIdx.y;
   const int cc = min(tile + (int)threadIdx.x, a.C - 1);  // the channel this thread sums
@@ -822,22 +825,38 @@ __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a
   } else {
     const int tokens = (int)a.tokens, chunk = (int)a.chunk;  // both, and all rows, below 2^31
     const int b0 = blockIdx.y * kGroupImages, b1 = min(b0 + kGroupImages, a.images);
-    const bool few = b1 - b0 <= kFewImages;
-    for (int b = few ? b0 : b0 + lane; b < b1; b += few ? 1 : kColLanes) {
-      const int s0 = tokens * b / chunk + b, s1 = a.ctas ? (tokens * (b + 1) - 1) / chunk + b : s0 - 1;
-      Sums v = slot_sum(a.part_post, s0 + (few ? lane : 0), s1, few ? kColLanes : 1, a.C, cc);
-      if (few) v = lane_sum(v, buf);
-      const int ch = few ? c : tile + (int)threadIdx.x;
-      if (ch < a.C) {
-        const float g = a.gate[(int64_t)b * a.C + ch];
-        all.one = fmaf(g, v.one, all.one);
-        all.zero = fmaf(g, v.zero, all.zero);
-        if (a.dgate && (!few || threadIdx.x == 0))
-          a.dgate[(int64_t)b * a.C + ch] =
-              a.kept * at(a.scale, ch, 1.f) * fmaf(at(gamma, ch, 1.f), v.one, at(beta, ch, 0.f) * v.zero);
+    auto slots = [&](int b, int &s0, int &s1) {
+      s0 = tokens * b / chunk + b;
+      s1 = a.ctas ? (tokens * (b + 1) - 1) / chunk + b : s0 - 1;
+    };
+    auto image = [&](int b, int ch, const Sums &v, bool store) {
+      if (ch >= a.C) return;
+      const float g = a.gate[(int64_t)b * a.C + ch];
+      all.one = fmaf(g, v.one, all.one);
+      all.zero = fmaf(g, v.zero, all.zero);
+      if (a.dgate && store)
+        a.dgate[(int64_t)b * a.C + ch] =
+            a.kept * at(a.scale, ch, 1.f) * fmaf(at(gamma, ch, 1.f), v.one, at(beta, ch, 0.f) * v.zero);
+    };
+    if (b1 - b0 <= kFewImages) {
+      Sums v[kFewImages];
+#pragma unroll
+      for (int k = 0; k < kFewImages; ++k) {
+        int s0 = 0, s1 = -1;
+        if (b0 + k < b1) slots(b0 + k, s0, s1);
+        v[k] = slot_sum(a.part_post, s0 + lane, s1, kColLanes, a.C, cc);
       }
+#pragma unroll
+      for (int k = 0; k < kFewImages; ++k)
+        if (b0 + k < b1) image(b0 + k, c, lane_sum(v[k], buf), threadIdx.x == 0);
+    } else {
+      for (int b = b0 + lane; b < b1; b += kColLanes) {
+        int s0, s1;
+        slots(b, s0, s1);
+        image(b, tile + (int)threadIdx.x, slot_sum(a.part_post, s0, s1, 1, a.C, cc), true);
+      }
+      all = lane_sum(all, buf);
     }
-    if (!few) all = lane_sum(all, buf);
   }
   if (!own) return;
   if (a.groups) {
@@ -1100,6 +1119,21 @@ int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, co
 
 namespace {
 
+// As a programmatic dependent of the kernel before it in the stream: its launch
+// overlaps that kernel's end (the fold took 10 us behind a backward of 80 us).
+int launch_columns(const ColArgs &c, int tiles, unsigned groups, cudaStream_t st) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles, groups, 2);
+  cfg.blockDim = dim3(32, kColLanes);
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, columns_kernel, c) == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
+}
+
 // Row pass and parameter gradients of the two backward entry points.
 int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_attn_join_grads &g, void *workspace,
                  size_t workspace_bytes, cudaStream_t st) {
@@ -1155,15 +1189,15 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   const int64_t groups = a.gate && want_post ? image_groups(a.images) : 1;
   if (groups > 65535) return SWIN_ERR_UNSUPPORTED;
   if (groups > 1) c.groups = a.part_post + join_slots(sp.ctas, a.images) * 2 * a.C;
-  columns_kernel<<<dim3(tiles, (unsigned)groups, 2), dim3(32, kColLanes), 0, st>>>(c);
+  if ((rc = launch_columns(c, tiles, (unsigned)groups, st))) return rc;
   if (groups > 1) {  // the groups' sums are what a join without a gate would have left
     c.part_post = c.groups;
     c.ctas = (int)groups;
     c.gate = nullptr;
     c.groups = c.dgate = c.dpre_gamma = c.dpre_beta = nullptr;
-    columns_kernel<<<dim3(tiles, 1, 2), dim3(32, kColLanes), 0, st>>>(c);
+    rc = launch_columns(c, tiles, 1, st);
   }
-  return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
+  return rc;
 }
 
 }  // namespace
