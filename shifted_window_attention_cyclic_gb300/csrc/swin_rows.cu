@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -958,11 +959,14 @@ Split split_rows(int64_t rows, int C, int sms, bool bwd, bool branch) {
   return {chunk, (int)((rows + chunk - 1) / chunk)};
 }
 
+// SMs of the current device (asked once per device: the calls are short).
 int sm_count(int *sms) {
+  static std::atomic<int> known[64];
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return SWIN_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return SWIN_ERR_CUDA;
+  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return SWIN_OK;
+  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SWIN_ERR_CUDA;
+  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
   return SWIN_OK;
 }
 

@@ -65,27 +65,23 @@ def check_dropout(name, drop, device):
         raise ValueError("%s: its state is on %s, expected %s" % (name, drop.state.tensor.device, device))
 
 
-class on:
-    """Make `device` (and `stream`, if given) current while outputs are
-    allocated and the call is issued, so that what the call allocates belongs
-    to the stream that uses it."""
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
+def on(device, stream):
+    """A context that makes `device` (and `stream`, if given) current while
+    outputs are allocated and the call is issued, so that what the call
+    allocates belongs to the stream that uses it; None where both are current."""
+    if stream is not None:
+        if stream.device != device:
             raise ValueError("stream: on %s, the tensors are on %s" % (stream.device, device))
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
+        return torch.cuda.stream(stream)
+    return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def same_rows(name, t, x):
+    """`t` is like the checked tensor `x`: shape, type, device, contiguous, aligned."""
+    if not (isinstance(t, torch.Tensor) and t.shape == x.shape and t.dtype == x.dtype and t.device == x.device
+            and t.is_contiguous() and t.data_ptr() % 16 == 0):
+        from .functional import check_tensor
+        check_tensor(name, t, x.shape, x.dtype, x.device)  # raises, saying which
 
 
 def apply_dropout(x, drop, span=1, out=None, stream=None):
@@ -93,21 +89,23 @@ def apply_dropout(x, drop, span=1, out=None, stream=None):
     the contiguous x). span = 1: dropout; tokens * channels: whole images
     (stochastic depth). The backward is the same call on the gradient. `out`
     may be x. drop = None copies."""
-    from .functional import check_tensor
     if not isinstance(x, torch.Tensor) or x.dtype not in _C_DTYPE:
         raise ValueError("x: expected a bfloat16 or float32 torch.Tensor")
     if not x.is_cuda:
         raise ValueError("x: on %s, expected a CUDA device" % x.device)
-    check_tensor("x", x, x.shape, x.dtype, x.device)
+    same_rows("x", x, x)
     if int(span) != span or span < 1:
         raise ValueError("span: at least 1, got %r" % (span,))
     if drop is not None:
         check_dropout("drop", drop, x.device)
     if out is not None:
-        check_tensor("out", out, x.shape, x.dtype, x.device)
-    with on(x.device, stream):
-        out = torch.empty_like(x) if out is None else out
-        C.swin_attn_dropout(_C_DTYPE[x.dtype], x.numel(), int(span), x, drop.desc if drop else None, out, stream)
+        same_rows("out", out, x)
+    ctx = on(x.device, stream)
+    if ctx is not None:
+        with ctx:
+            return apply_dropout(x, drop, span, out)
+    out = torch.empty_like(x) if out is None else out
+    C.swin_attn_dropout(_C_DTYPE[x.dtype], x.numel(), int(span), x, drop.desc if drop else None, out)
     return out
 
 

@@ -130,8 +130,13 @@ class SwinWindowAttention:
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
         if dbias is None and want_dbias:
-            dbias = self.new_bias()
-        ws = self.workspace()  # dBias partial tables; for head_dim 128 also delta
+            dbias = torch.empty(self.bias_shape, dtype=torch.float32, device=self.device)  # overwritten
+        if drop is not None:
+            # a workspace of the call's own, on its stream: calls and captured graphs may overlap
+            with torch.cuda.stream(stream):
+                ws = torch.empty(max(C.swin_attn_workspace_bytes(self.plan), 256), dtype=torch.uint8, device=self.device)
+        else:
+            ws = self.workspace()  # dBias partial tables; for head_dim 128 also delta
         if drop is not None:
             C.swin_attn_bwd_dropout(self.plan, q, k, v, o, dout, lse, bias, land if self.has_land else None, dq, dk, dv,
                                     dbias, ws, drop, stream)

@@ -11,15 +11,18 @@ is saved.
 """
 from __future__ import annotations
 
+import math
 from collections import namedtuple
 
 import torch
 
 from . import swin_attn as C
-from .dropout import check_dropout, on
+from .dropout import check_dropout, on, same_rows
 from .functional import _TORCH_DTYPE, check_tensor
 
 _KINDS = {"none": C.SWIN_NORM_NONE, "layer": C.SWIN_NORM_LAYER, "rms": C.SWIN_NORM_RMS}
+
+_NO_DROP = C.swin_attn_drop(0.0, 0, None)
 
 JoinGrads = namedtuple("JoinGrads", "dx dz dpost_gamma dpost_beta dscale dgate dpre_gamma dpre_beta")
 
@@ -33,7 +36,7 @@ def _check_param(name, t, shape, device):
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
-    if tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
         raise ValueError("%s: want a contiguous float32 %s on %s" % (name, tuple(shape), device))
 
 
@@ -49,6 +52,7 @@ class _Rows:
             raise ValueError("eps: positive and finite, got %r" % (eps,))
         self.channels, self.eps, self.dtype = int(channels), float(eps), dtype
         self.torch_dtype = _TORCH_DTYPE[dtype]
+        self.c_dtype = C.SWIN_BF16 if dtype == "bf16" else C.SWIN_F32
 
     def _rows(self, name, x):
         """Check the call's first tensor [B, *grid, C]; its descriptor."""
@@ -58,17 +62,16 @@ class _Rows:
             raise ValueError("%s: on %s, expected a CUDA device" % (name, x.device))
         if x.dim() < 2 or x.shape[-1] != self.channels:
             raise ValueError("%s: shape %s, expected [B, *grid, %d]" % (name, tuple(x.shape), self.channels))
-        check_tensor(name, x, x.shape, self.torch_dtype, x.device)
-        images = x.shape[0]
-        tokens = 1
-        for g in x.shape[1:-1]:
-            tokens *= g
-        return C.swin_attn_rows(images, tokens, self.channels, C.SWIN_BF16 if self.dtype == "bf16" else C.SWIN_F32)
+        if x.dtype != self.torch_dtype or not x.is_contiguous() or x.data_ptr() % 16:
+            check_tensor(name, x, x.shape, self.torch_dtype, x.device)  # raises, saying which
+        images, *grid = x.shape[:-1]
+        return C.swin_attn_rows(images, math.prod(grid), self.channels, self.c_dtype)
 
-    def _same(self, x, **tensors):
+    @staticmethod
+    def _same(x, **tensors):
         for name, t in tensors.items():
             if t is not None:
-                check_tensor(name, t, x.shape, self.torch_dtype, x.device)
+                same_rows(name, t, x)
 
     @staticmethod
     def _workspace(rows, device):
@@ -94,9 +97,12 @@ class BlockNorm(_Rows):
         """h = N(x); `h` may be x."""
         rows, norm = self._rows("x", x), self._norm(x, gamma, beta)
         self._same(x, h=h)
-        with on(x.device, stream):
-            h = torch.empty_like(x) if h is None else h
-            C.swin_attn_norm_fwd(rows, x, norm, h, stream)
+        ctx = on(x.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.forward(x, gamma, beta, h)
+        h = torch.empty_like(x) if h is None else h
+        C.swin_attn_norm_fwd(rows, x, norm, h)
         return h
 
     def backward(self, x, dh, gamma=None, beta=None, dres=None, dx=None, want_params=True, stream=None):
@@ -107,12 +113,15 @@ class BlockNorm(_Rows):
         if dh is None:
             raise ValueError("dh: the backward needs the gradient of h")
         self._same(x, dh=dh, dres=dres, dx=dx)
-        with on(x.device, stream):
-            dx = torch.empty_like(x) if dx is None else dx
-            dgamma = torch.empty_like(gamma) if want_params and gamma is not None else None
-            dbeta = torch.empty_like(beta) if want_params and beta is not None else None
-            ws = self._workspace(rows, x.device) if dgamma is not None or dbeta is not None else None
-            C.swin_attn_norm_bwd(rows, x, norm, dh, dres, dx, dgamma, dbeta, ws, stream)
+        ctx = on(x.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.backward(x, dh, gamma, beta, dres, dx, want_params)
+        dx = torch.empty_like(x) if dx is None else dx
+        dgamma = torch.empty_like(gamma) if want_params and gamma is not None else None
+        dbeta = torch.empty_like(beta) if want_params and beta is not None else None
+        ws = self._workspace(rows, x.device) if dgamma is not None or dbeta is not None else None
+        C.swin_attn_norm_bwd(rows, x, norm, dh, dres, dx, dgamma, dbeta, ws)
         return dx, dgamma, dbeta
 
 
@@ -140,13 +149,12 @@ class ResidualJoin(_Rows):
             _check_param(name, t, c, dev)
         _check_param("scale", scale, c, dev)
         _check_param("gate", gate, (x.shape[0],) + c, dev)
-        none = C.swin_attn_drop(0.0, 0, None)
         for name, d in (("drop", drop), ("path", path)):
             if d is not None:
                 check_dropout(name, d, dev)
         return C.swin_attn_join(C.swin_attn_norm(_KINDS[self.post], self.eps, _addr(post_gamma), _addr(post_beta)),
                                 C.swin_attn_norm(_KINDS[self.pre], self.eps, _addr(pre_gamma), _addr(pre_beta)),
-                                _addr(scale), _addr(gate), drop.desc if drop else none, path.desc if path else none)
+                                _addr(scale), _addr(gate), drop.desc if drop else _NO_DROP, path.desc if path else _NO_DROP)
 
     def forward(self, x, z, post_gamma=None, post_beta=None, scale=None, gate=None, pre_gamma=None, pre_beta=None,
                 drop=None, path=None, y=None, h=None, stream=None):
@@ -157,11 +165,15 @@ class ResidualJoin(_Rows):
         self._same(x, z=z, y=y, h=h)
         if h is not None and self.pre == "none":
             raise ValueError("h: the join has no pre norm")
-        join = self._join(x, post_gamma, post_beta, scale, gate, pre_gamma, pre_beta, drop, path)
-        with on(x.device, stream):
-            y = torch.empty_like(x) if y is None else y
-            h = torch.empty_like(x) if h is None and self.pre != "none" else h
-            C.swin_attn_join_fwd(rows, x, z, join, y, h, stream)
+        params = (post_gamma, post_beta, scale, gate, pre_gamma, pre_beta, drop, path)
+        join = self._join(x, *params)
+        ctx = on(x.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.forward(x, z, *params, y, h)
+        y = torch.empty_like(x) if y is None else y
+        h = torch.empty_like(x) if h is None and self.pre != "none" else h
+        C.swin_attn_join_fwd(rows, x, z, join, y, h)
         return y, h
 
     def backward(self, y, z, dy, dh=None, post_gamma=None, post_beta=None, scale=None, gate=None, pre_gamma=None,
@@ -177,15 +189,17 @@ class ResidualJoin(_Rows):
         if z is None:
             raise ValueError("z: the backward needs the block's output")
         self._same(y, z=z, dy=dy, dh=dh)
-        join = self._join(y, post_gamma, post_beta, scale, gate, pre_gamma, pre_beta, drop, path)
-        with on(y.device, stream):
-            dx, dz = torch.empty_like(y), torch.empty_like(y)
-            params = [torch.empty_like(p) if want_params and p is not None else None
-                      for p in (post_gamma, post_beta, scale, gate, pre_gamma, pre_beta)]
-            ws = self._workspace(rows, y.device) if any(p is not None for p in params) else None
-            C.swin_attn_join_bwd(rows, y, z, join, dy, dh, dx, dz, C.swin_attn_join_grads(*map(_addr, params)), ws,
-                                 stream)
-        return JoinGrads(dx, dz, *params)
+        params = (post_gamma, post_beta, scale, gate, pre_gamma, pre_beta)
+        join = self._join(y, *params, drop, path)
+        ctx = on(y.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.backward(y, z, dy, dh, *params, drop, path, want_params)
+        dx, dz = torch.empty_like(y), torch.empty_like(y)
+        grads = [torch.empty_like(p) if want_params and p is not None else None for p in params]
+        ws = self._workspace(rows, y.device) if any(g is not None for g in grads) else None
+        C.swin_attn_join_bwd(rows, y, z, join, dy, dh, dx, dz, C.swin_attn_join_grads(*map(_addr, grads)), ws)
+        return JoinGrads(dx, dz, *grads)
 
 
 class _NormFn(torch.autograd.Function):

@@ -303,7 +303,7 @@ def swin_attn_bwd_o(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, d
 def swin_attn_fwd_dropout(plan: Plan, q, k, v, bias, land, o, lse, drop: swin_attn_drop, stream=None) -> None:
     pq, pk, pv, po, plse = _acts(("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse))
     _check(load_library().swin_attn_fwd_dropout(plan.handle, pq, pk, pv, _ptr(bias, 4, "bias"),
-                                                _ptr(land, 4, "land"), po, plse, drop, _stream(stream)),
+                                                _ptr(land, 4, "land"), po, plse, drop, _handle(stream)),
            "swin_attn_fwd_dropout")
 
 
@@ -315,32 +315,41 @@ def swin_attn_bwd_dropout(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk,
                                                      ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv))
     _check(load_library().swin_attn_bwd_dropout(plan.handle, pq, pk, pv, po, pdo, plse, _ptr(bias, 4, "bias"),
                                                 _ptr(land, 4, "land"), pdq, pdk, pdv, _ptr(dbias, 4, "dbias"),
-                                                _ptr(workspace, 256, "workspace"), ws_bytes, drop, _stream(stream)),
+                                                _ptr(workspace, 256, "workspace"), ws_bytes, drop, _handle(stream)),
            "swin_attn_bwd_dropout")
-
-
-def swin_attn_rows_workspace_bytes(rows: swin_attn_rows) -> int:
-    return int(load_library().swin_attn_rows_workspace_bytes(rows))
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _handle(stream):
+    """cudaStream_t of `stream`, or of the current stream, as a whole number
+    (short: the row calls are often shorter on the GPU than their host code)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def swin_attn_rows_workspace_bytes(rows: swin_attn_rows) -> int:
+    return load_library().swin_attn_rows_workspace_bytes(rows)
+
+
 def swin_attn_norm_fwd(rows: swin_attn_rows, x, norm: swin_attn_norm, h, stream=None) -> None:
-    _check(load_library().swin_attn_norm_fwd(rows, _addr(x), norm, _addr(h), _stream(stream)), "swin_attn_norm_fwd")
+    _check(load_library().swin_attn_norm_fwd(rows, _addr(x), norm, _addr(h), _handle(stream)), "swin_attn_norm_fwd")
 
 
 def swin_attn_norm_bwd(rows: swin_attn_rows, x, norm: swin_attn_norm, dh, dres, dx, dgamma, dbeta, workspace,
                        stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().swin_attn_norm_bwd(rows, _addr(x), norm, _addr(dh), _addr(dres), _addr(dx), _addr(dgamma),
-                                             _addr(dbeta), _addr(workspace), ws_bytes, _stream(stream)),
+                                             _addr(dbeta), _addr(workspace), ws_bytes, _handle(stream)),
            "swin_attn_norm_bwd")
 
 
 def swin_attn_join_fwd(rows: swin_attn_rows, x, z, join: swin_attn_join, y, h, stream=None) -> None:
-    _check(load_library().swin_attn_join_fwd(rows, _addr(x), _addr(z), join, _addr(y), _addr(h), _stream(stream)),
+    _check(load_library().swin_attn_join_fwd(rows, _addr(x), _addr(z), join, _addr(y), _addr(h), _handle(stream)),
            "swin_attn_join_fwd")
 
 
@@ -348,12 +357,12 @@ def swin_attn_join_bwd(rows: swin_attn_rows, y, z, join: swin_attn_join, dy, dh,
                        workspace, stream=None) -> None:
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().swin_attn_join_bwd(rows, _addr(y), _addr(z), join, _addr(dy), _addr(dh), _addr(dx),
-                                             _addr(dz), grads, _addr(workspace), ws_bytes, _stream(stream)),
+                                             _addr(dz), grads, _addr(workspace), ws_bytes, _handle(stream)),
            "swin_attn_join_bwd")
 
 
 def swin_attn_dropout(dtype: int, n: int, span: int, x, drop: swin_attn_drop, y, stream=None) -> None:
-    _check(load_library().swin_attn_dropout(dtype, n, span, _addr(x), drop, _addr(y), _stream(stream)),
+    _check(load_library().swin_attn_dropout(dtype, n, span, _addr(x), drop, _addr(y), _handle(stream)),
            "swin_attn_dropout")
 
 
