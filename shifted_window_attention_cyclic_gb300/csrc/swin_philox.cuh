@@ -133,20 +133,17 @@ __device__ __forceinline__ uint32_t group_bits(const uint4 &a, const uint4 &b, c
   }
   return bits;
 }
-// 0xFFFF in the halves that keep, 0 in the others, of keys e and e + 1 (e even) of
-// the group whose bits start at bit `at` (0 or 4) of the word's bytes.
-__device__ __forceinline__ uint32_t keep_mask(uint32_t word, int at, int e) {
+// 0xFFFF in the halves that keep, 0 in the others, of keys e and e + 1 (e even) of a group.
+__device__ __forceinline__ uint32_t keep_mask(uint32_t bits, int e) {
   uint32_t m;
   if (e & 2)
-    asm("prmt.b32 %0, %1, 0, 0xBBAA;" : "=r"(m) : "r"(word << (7 - at - (e >> 2))));
+    asm("prmt.b32 %0, %1, 0, 0xBBAA;" : "=r"(m) : "r"(bits << (7 - (e >> 2))));
   else
-    asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m) : "r"(word << (7 - at - (e >> 2))));
+    asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m) : "r"(bits << (7 - (e >> 2))));
   return m;
 }
-// Key e of that group alone.
-__device__ __forceinline__ bool keep_bit(uint32_t word, int at, int e) {
-  return (word & (1u << (8 * (e & 3) + at + (e >> 2)))) != 0u;
-}
+// Key e of a group alone.
+__device__ __forceinline__ bool keep_bit(uint32_t bits, int e) { return (bits & (1u << (8 * (e & 3) + (e >> 2)))) != 0u; }
 
 // A block's eight decisions, bit e = decision e keeps.
 __device__ __forceinline__ uint32_t keep_bits(const uint4 &u, uint32_t thr) {

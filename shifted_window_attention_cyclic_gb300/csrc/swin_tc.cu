@@ -483,9 +483,8 @@ __device__ __forceinline__ void gather_role(const Geo &g, const StageLayout &lay
   }
 }
 
-// Dropout decisions of a softmax thread's half row (its warpgroup's keys, in
-// 16-key groups from its first): group k has its bits (group_bits) in word k / 2,
-// at bits 4 * (k % 2) of the bytes.
+// Dropout decisions of a softmax thread's half row (its warpgroup's keys), one
+// 16-key group (two generator blocks) at a time.
 struct KeepDraw {
   Philox ph;
   PairTest test;
@@ -496,27 +495,16 @@ struct KeepDraw {
     nb = (g.n + 7) >> 3;
     first = first_block;
   }
-  // One group, two generator blocks, a trip of a rolled loop: on the 256 x 540
-  // stage (16 heads, 96 slots) the forward takes 351 us and the backward 572 us,
-  // against 216 and 448 us without dropout (of the difference, 20 and 60 us are
-  // the use of the bits). The roles' code together is larger than the
-  // instruction caches, so shorter code wins: two groups a trip took 390 / 588 us,
-  // unrolled by two 384 / 613 us, rolled rounds 408 / 613 us, drawn beside the
-  // exponentials 348 / 650 us. Drawn by the epilogue warps, one bit per key
-  // through shared memory, it took 351 / 608 us (those warps have no idle time),
-  // by four more warps with the registers split over the roles 519 / 767 us.
-  __device__ __forceinline__ uint2 half_row(const Geo &g, const ItemCursor &x, int src, int groups) const {
-    uint64_t b = (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + first;
-    uint2 w = make_uint2(0u, 0u);
-#pragma unroll 1
-    for (int k = 0; k < groups; ++k, b += 2) {
-      const uint64_t at[2] = {b, b + 1};
-      uint4 r[2];
-      ph.blocks(at, r);
-      const uint32_t bits = group_bits(r[0], r[1], test) << (4 * (k & 1));
-      if (k < 2) w.x |= bits; else w.y |= bits;
-    }
-    return w;
+  // the half row's first block, of the row of query token src (negative: a pad, any row will do)
+  __device__ __forceinline__ uint64_t block(const Geo &g, const ItemCursor &x, int src) const {
+    return (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + first;
+  }
+  // the group whose first block is b (group_bits)
+  __device__ __forceinline__ uint32_t group(uint64_t b) const {
+    const uint64_t at[2] = {b, b + 1};
+    uint4 r[2];
+    ph.blocks(at, r);
+    return group_bits(r[0], r[1], test);
   }
 };
 
@@ -568,9 +556,9 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 
 // kPack: windows per work item (1 or 2), a compile-time copy per value so
 // that the one-window kernel carries no code for the second window.
-// kDrop: dropout of the probabilities. A softmax thread draws its half row's
-// decisions while S is computed and ANDs them onto packed P; the row sums are
-// taken before, and the kept values' scale goes into the epilogue's 1 / l.
+// kDrop: dropout of the probabilities. A softmax thread draws its row's decisions
+// beside the exponentials and ANDs them onto packed P; the row sums are taken
+// before, and the kept values' scale goes into the epilogue's 1 / l.
 template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_tc_kernel(const FwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
@@ -871,11 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int wb = (int)(it & 1), xs = (int)(it % kXchgSlots);
       const uint32_t tS = tmem + lane_addr + kColS + 128u * wb;
-      uint2 keep = make_uint2(0u, 0u);  // this half row's decisions
-      if (kDrop && !idle) {
+      uint64_t blk = 0;  // this half row's first generator block
+      if (kDrop) {       // (the stage is held until P is written)
         const int s = (int)(it % kStages);
         if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
-        keep = draw.half_row(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i], ge - gb);
+        blk = draw.block(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i]);
       }
       if (!mbar_wait_warp(bar(bSFull + wb), (uint32_t)(it >> 1) & 1u, ctl)) break;
       tc_fence_after();
@@ -891,51 +879,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_warp(bar(bPFull + wb));
         continue;
       }
-      uint32_t sv[4][16];
-#pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4)
-        if (gb + k4 < ge) tmem_ld16(tS + 16u * (gb + k4), sv[k4]);
-      tmem_wait_ld_tied(sv[0], sv[1]);
-      tmem_wait_ld_tied(sv[2], sv[3]);
-      // x = S*cs + bias2 (kept in sv), half row max (independent chains)
-      float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        if (gb + k4 < ge) {
+      float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, m;
+      float2 sp2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      if constexpr (kDrop) {
+        // The same arithmetic in two rolled passes of one 16-key group a trip, x
+        // going back over S in between: all roles' code together outgrows the
+        // instruction caches, and with the generator's in it the unrolled form
+        // below took 351 us on the 256 x 540 stage (16 heads, 96 slots) with the
+        // decisions drawn ahead, 348 us drawn beside the exponentials; this one
+        // 289 us (two groups a trip 345 us; without dropout 216 us, 210 us in
+        // this form, which is 3 % slower on 128-slot windows).
+        uint32_t sv[16];
+#pragma unroll 1
+        for (int gi = gb; gi < ge; ++gi) {
+          tmem_ld16(tS + 16u * gi, sv);
+          tmem_wait_ld_tied(sv);
 #pragma unroll
           for (int e4 = 0; e4 < 16; e4 += 4) {
-            const float4 b4 = *reinterpret_cast<const float4 *>(brow + 16 * (gb + k4) + e4);
-            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(sv[k4][e4]), __uint_as_float(sv[k4][e4 + 1])),
-                                         cs2, make_float2(b4.x, b4.y));
-            const float2 x1 = __ffma2_rn(
-                make_float2(__uint_as_float(sv[k4][e4 + 2]), __uint_as_float(sv[k4][e4 + 3])), cs2,
-                make_float2(b4.z, b4.w));
-            sv[k4][e4] = __float_as_uint(x0.x);
-            sv[k4][e4 + 1] = __float_as_uint(x0.y);
-            sv[k4][e4 + 2] = __float_as_uint(x1.x);
-            sv[k4][e4 + 3] = __float_as_uint(x1.y);
+            const float4 b4 = *reinterpret_cast<const float4 *>(brow + 16 * gi + e4);
+            const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(sv[e4]), __uint_as_float(sv[e4 + 1])), cs2,
+                                         make_float2(b4.x, b4.y));
+            const float2 x1 = __ffma2_rn(make_float2(__uint_as_float(sv[e4 + 2]), __uint_as_float(sv[e4 + 3])), cs2,
+                                         make_float2(b4.z, b4.w));
+            sv[e4] = __float_as_uint(x0.x);
+            sv[e4 + 1] = __float_as_uint(x0.y);
+            sv[e4 + 2] = __float_as_uint(x1.x);
+            sv[e4 + 3] = __float_as_uint(x1.y);
             mp[e4 >> 2] = max3(mp[e4 >> 2], max3(x0.x, x0.y, x1.x), x1.y);
           }
+          tmem_st16(tS + 16u * gi, sv);
         }
-      }
-      const float m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-      // p = exp2(x - m), half row sum, P (bf16) over S
-      const float2 negm = make_float2(-m, -m);
-      float2 sp2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int k4 = 0; k4 < 4; ++k4) {
-        if (gb + k4 < ge) {
+        m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+        const float2 negm = make_float2(-m, -m);
+        tmem_wait_st();
+#pragma unroll 1
+        for (int gi = gb; gi < ge; ++gi, blk += 2) {
+          tmem_ld16(tS + 16u * gi, sv);
+          const uint32_t keep = draw.group(blk);
+          tmem_wait_ld_tied(sv);
           uint32_t pv[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float2 xs2 =
-                __fadd2_rn(make_float2(__uint_as_float(sv[k4][e]), __uint_as_float(sv[k4][e + 1])), negm);
+            const float2 xs2 = __fadd2_rn(make_float2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), negm);
             const float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
             sp2[(e >> 1) & 3] = __fadd2_rn(sp2[(e >> 1) & 3], p);
-            pv[e >> 1] = pack_bf16(p.x, p.y);
-            if (kDrop) pv[e >> 1] &= keep_mask(k4 < 2 ? keep.x : keep.y, 4 * (k4 & 1), e);
+            pv[e >> 1] = pack_bf16(p.x, p.y) & keep_mask(keep, e);
           }
-          tmem_st8(tS + 16u * (gb + k4), pv);  // over the first half of its own S group
+          tmem_st8(tS + 16u * gi, pv);  // over the first half of its own S group
+        }
+      } else {
+        uint32_t sv[4][16];
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4)
+          if (gb + k4 < ge) tmem_ld16(tS + 16u * (gb + k4), sv[k4]);
+        tmem_wait_ld_tied(sv[0], sv[1]);
+        tmem_wait_ld_tied(sv[2], sv[3]);
+        // x = S*cs + bias2 (kept in sv), half row max (independent chains)
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          if (gb + k4 < ge) {
+#pragma unroll
+            for (int e4 = 0; e4 < 16; e4 += 4) {
+              const float4 b4 = *reinterpret_cast<const float4 *>(brow + 16 * (gb + k4) + e4);
+              const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(sv[k4][e4]), __uint_as_float(sv[k4][e4 + 1])),
+                                           cs2, make_float2(b4.x, b4.y));
+              const float2 x1 = __ffma2_rn(
+                  make_float2(__uint_as_float(sv[k4][e4 + 2]), __uint_as_float(sv[k4][e4 + 3])), cs2,
+                  make_float2(b4.z, b4.w));
+              sv[k4][e4] = __float_as_uint(x0.x);
+              sv[k4][e4 + 1] = __float_as_uint(x0.y);
+              sv[k4][e4 + 2] = __float_as_uint(x1.x);
+              sv[k4][e4 + 3] = __float_as_uint(x1.y);
+              mp[e4 >> 2] = max3(mp[e4 >> 2], max3(x0.x, x0.y, x1.x), x1.y);
+            }
+          }
+        }
+        m = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
+        // p = exp2(x - m), half row sum, P (bf16) over S
+        const float2 negm = make_float2(-m, -m);
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) {
+          if (gb + k4 < ge) {
+            uint32_t pv[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float2 xs2 =
+                  __fadd2_rn(make_float2(__uint_as_float(sv[k4][e]), __uint_as_float(sv[k4][e + 1])), negm);
+              const float2 p = make_float2(ex2(xs2.x), ex2(xs2.y));
+              sp2[(e >> 1) & 3] = __fadd2_rn(sp2[(e >> 1) & 3], p);
+              pv[e >> 1] = pack_bf16(p.x, p.y);
+            }
+            tmem_st8(tS + 16u * (gb + k4), pv);  // over the first half of its own S group
+          }
         }
       }
       const float2 sum2 = __fadd2_rn(__fadd2_rn(sp2[0], sp2[1]), __fadd2_rn(sp2[2], sp2[3]));
@@ -1311,22 +1346,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         cur_h = x.h;
       }
       const int s = (int)(it % kStages);
-      uint2 keep = make_uint2(0u, 0u);  // this half row's decisions
-      if (kDrop && !idle) {
-        if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
-        keep = draw.half_row(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i], ge - gb);
-      }
       if (!mbar_wait_warp(bar(bSpFull), (uint32_t)it & 1u, ctl)) break;
       tc_fence_after();
       if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
       const uint8_t *sp = smem + s * kStageBytes;
       const float lse2 = reinterpret_cast<const float *>(sp + kMeta + 512)[i];
       const bool live = (sp + kMeta + 1024)[i] != 0;
+      uint64_t blk = 0;  // this half row's first generator block
+      if (kDrop) blk = draw.block(g, x, reinterpret_cast<const int *>(sp + kMeta)[i]);
       // pass 1: P = exp2(S*cs + bias2 - lse2); partial delta = sum_j P dP over
       // this half; P (fp32) back over S in TMEM, P (bf16) to the smem tile.
       float delta = 0.f;
       const float2 nl2 = make_float2(-lse2, -lse2);
-      auto p_group = [&](int gi, uint32_t (&sv)[16], uint32_t (&dpv)[16], uint32_t kw, int at) {
+      auto p_group = [&](int gi, uint32_t (&sv)[16], uint32_t (&dpv)[16], uint32_t keep) {
         uint32_t pb[8];
 #pragma unroll
         for (int e4 = 0; e4 < 16; e4 += 4) {
@@ -1339,15 +1371,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             xs = __fadd2_rn(xs, nl2);
             const float p0 = live ? ex2(xs.x) : 0.f, p1 = live ? ex2(xs.y) : 0.f;
             if (kDrop) {
-              dpv[e] = keep_bit(kw, at, e) ? dpv[e] : 0u;
-              dpv[e + 1] = keep_bit(kw, at, e + 1) ? dpv[e + 1] : 0u;
+              dpv[e] = keep_bit(keep, e) ? dpv[e] : 0u;
+              dpv[e + 1] = keep_bit(keep, e + 1) ? dpv[e + 1] : 0u;
             }
             delta = fmaf(p0, __uint_as_float(dpv[e]), delta);
             delta = fmaf(p1, __uint_as_float(dpv[e + 1]), delta);
             sv[e] = __float_as_uint(p0);  // P (fp32) overwrites S in the register buffer
             sv[e + 1] = __float_as_uint(p1);
             pb[e >> 1] = pack_bf16(p0, p1);
-            if (kDrop) pb[e >> 1] &= keep_mask(kw, at, e);
+            if (kDrop) pb[e >> 1] &= keep_mask(keep, e);
           }
         }
         tmem_st16(tS + 16u * gi, sv);
@@ -1357,6 +1389,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (idle) {
         zero_chunks(kP);
+      } else if (kDrop) {
+        // one group a trip, its decisions drawn while S and dP arrive
+        uint32_t s0[16], d0[16];
+#pragma unroll 1
+        for (int gi = gb; gi < ge; ++gi, blk += 2) {
+          tmem_ld16(tS + 16u * gi, s0);
+          tmem_ld16(tdP + 16u * gi, d0);
+          const uint32_t keep = draw.group(blk);
+          tmem_wait_ld_tied(s0, d0);
+          p_group(gi, s0, d0, keep);
+        }
       } else {
         // two groups per TMEM round trip: tcgen05.wait::ld waits for every
         // load in flight, so a double buffer would wait just as often, and
@@ -1373,10 +1416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_ld16(tdP + 16u * g1, d1);
             }
             tmem_wait_ld_tied(s0, d0);
-            p_group(g0, s0, d0, k2 ? keep.y : keep.x, 0);
+            p_group(g0, s0, d0, 0u);
             if (g1 < ge) {
               tmem_tie(s1, d1);
-              p_group(g1, s1, d1, k2 ? keep.y : keep.x, 4);
+              p_group(g1, s1, d1, 0u);
             }
           }
         }
