@@ -200,7 +200,6 @@ int swin_attn_bwd_o(swin_attn_plan_t plan, const void *q, const void *k, const v
  * the log-sum-exp is the softmax's, without dropout. Decision of query token
  * t (of image b, head h) and key slot j of its window of n slots:
  * 8 * (r * ceil(n / 8)) + j with r = (b * heads + h) * tokens + t.
- * head_dim 16 and 32 (head_dim 128 with a rate: UNSUPPORTED).
  * Errors: those of swin_attn_fwd. */
 int swin_attn_fwd_dropout(swin_attn_plan_t plan, const void *q, const void *k, const void *v, const float *bias,
                           const uint8_t *land, void *o, float *lse, const swin_attn_drop *drop,

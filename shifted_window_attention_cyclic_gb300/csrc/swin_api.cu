@@ -371,7 +371,6 @@ int fwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
   FwdArgs a;
   int rc = make_drop(drop, &a.drop);
   if (rc) return rc;
-  if (a.drop.thr && p->large) return SWIN_ERR_UNSUPPORTED;  // the key-tiled kernels have no dropout
   rc = current_device_matches(p);
   if (rc) return rc;
   a.g = p->g;
@@ -413,7 +412,6 @@ int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
   BwdArgs a;
   int rc = make_drop(drop, &a.drop);
   if (rc) return rc;
-  if (a.drop.thr && p->large) return SWIN_ERR_UNSUPPORTED;  // the key-tiled kernels have no dropout
   rc = current_device_matches(p);
   if (rc) return rc;
   a.g = p->g;
@@ -447,7 +445,7 @@ int bwd_impl(swin_attn_plan_t p, const void *q, const void *k, const void *v, co
   f.dbias = dbias;
   f.T = p->g.T;
   f.heads = p->g.heads;
-  f.scale = a.drop.scale;  // the kernels leave the kept values' scale out of dS
+  f.scale = p->large ? 1.f : a.drop.scale;  // the small-window kernels leave the kept values' scale out of dS
   const int total = f.T * f.heads;
   fold_kernel<<<(total + 255) / 256, 256, 0, static_cast<cudaStream_t>(stream)>>>(f);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;

@@ -631,6 +631,11 @@ int launch_block_fwd(const BlockArgs &a, const void *w_qkv, const void *w_o, voi
   const Geo &g = a.g;
   if (g.hd != blk::kHdB || g.n > 128 || g.C % 64 != 0 || g.C > blk::kMaxC || g.heads * g.T > blk::kMaxBias)
     return SWIN_ERR_UNSUPPORTED;
+  // (before the tensor maps: a thread's first runtime call binds the device's
+  // context, which encoding them needs and does not do)
+  if (cudaFuncSetAttribute(blk::block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, blk::kSmemBytes) !=
+      cudaSuccess)
+    return SWIN_ERR_CUDA;
   PFN_cuTensorMapEncodeTiled_v12000 enc = lg::tensor_map_encoder();
   if (!enc) return SWIN_ERR_CUDA;
   CUtensorMap mq, mo;
@@ -672,9 +677,6 @@ int launch_block_fwd(const BlockArgs &a, const void *w_qkv, const void *w_o, voi
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return SWIN_ERR_CUDA;
   }
-  if (cudaFuncSetAttribute(blk::block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, blk::kSmemBytes) !=
-      cudaSuccess)
-    return SWIN_ERR_CUDA;
   blk::block_kernel<<<a.ctas, blk::kThreads, blk::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mo, mx, my);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }

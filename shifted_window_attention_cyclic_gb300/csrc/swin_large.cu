@@ -108,7 +108,10 @@ __device__ __forceinline__ LItem decode_pair(const Geo &g, int64_t it) {
 
 // kRuns: key/value tiles load runs of slots as boxes (windows of at least
 // kRunMinKeyTiles key tiles); otherwise every row by gather4.
-template <bool kRuns>
+// kDrop: dropout of the probabilities. A softmax thread draws its row's decisions
+// for 64 keys at a time (four groups in a rolled loop) and ANDs them onto packed
+// P; the row sums are taken before, and the kept values' scale goes into 1 / l.
+template <bool kRuns, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_large_kernel(const FwdArgs a, const __grid_constant__ TileMaps tmq, const __grid_constant__ TileMaps tmk,
                      const __grid_constant__ TileMaps tmv) {
@@ -336,6 +339,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool live = false, mine = false;
     float bmax2 = 0.f, m_run = -INFINITY, l_run = 0.f;
     uint32_t bs_phase = 0, nt = 0;  // key tiles of this warpgroup's query tiles so far (barrier phases)
+    KeepDraw draw;
+    if (kDrop) draw.init(a.drop, g.n);
+    uint64_t blk0 = 0;  // the row's first generator block
     bool ok = true;
     auto bsync = [&]() -> bool {
       mbar_arrive_warp(bar(bBsync));
@@ -375,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         src = mine && slot < g.n ? r.src : -1;
         rbase = mine && slot < g.n ? r.rbase : g.T - 1;
         live = src >= 0 && (!a.land || __ldg(a.land + (int64_t)x.b * g.tokens + src) == 0);
+        if (kDrop) blk0 = draw.row(x.b, x.h, g.heads, g.tokens, src);
         m_run = -INFINITY;
         l_run = 0.f;
       }
@@ -485,6 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        uint32_t keep[2] = {0u, 0u};  // groups 0-1, 2-3 of the 64 keys, at bits 0-3 and 4-7 of the bytes
+        if (kDrop) {
+          uint64_t b = blk0 + 16u * kt + 8u * c;
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k, b += 2) {
+            const uint32_t bits = draw.group(b) << (4 * (k & 1));
+            if (k < 2) keep[0] |= bits; else keep[1] |= bits;
+          }
+        }
         // P = exp2(x - m) in bf16 over S, row sum
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
@@ -495,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : make_float2(0.f, 0.f);
             sp2[(e >> 1) & 1] = __fadd2_rn(sp2[(e >> 1) & 1], p);
             pv[e >> 1] = pack_bf16(p.x, p.y);
+            if (kDrop) pv[e >> 1] &= keep_mask(keep[k4 >> 1] >> (4 * (k4 & 1)), e);
           }
           tmem_st8(tS + 64u * c + 16u * k4, pv);
         }
@@ -509,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // epilogue of the item: O / l at the query tokens, the log-sum-exp
         if (!mbar_wait_warp(bar(bPVDone + xq), (nt - 1) & 1u, ctl)) break;
         tc_fence_after();
-        const float inv = live && l_run > 0.f ? __frcp_rn(l_run) : 0.f;
+        const float inv = live && l_run > 0.f ? (kDrop ? a.drop.scale * __frcp_rn(l_run) : __frcp_rn(l_run)) : 0.f;
         const bool store = src >= 0 && in_bounds(((int64_t)x.b * g.tokens + src) * g.C + (int64_t)x.h * kHd, kHd,
                                                   (int64_t)g.batch * g.tokens * g.C, a.status);
         uint4 *dst = store ? reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) +
@@ -558,11 +575,15 @@ int64_t large_fwd_items(const Geo &g) { return (int64_t)g.heads * g.batch * g.nw
 int launch_fwd_large(const FwdArgs &a, void *stream) {
   if (a.bias && a.g.T > lg::kMaxBiasRows) return SWIN_ERR_UNSUPPORTED;
   lg::TileMaps mq, mk, mv;
-  if (!lg::tile_maps(&mq, a.q, a.g) || !lg::tile_maps(&mk, a.k, a.g) || !lg::tile_maps(&mv, a.v, a.g))
-    return SWIN_ERR_CUDA;
-  auto kern = a.g.nqt >= lg::kRunMinKeyTiles ? lg::fwd_large_kernel<true> : lg::fwd_large_kernel<false>;
+  const bool runs = a.g.nqt >= lg::kRunMinKeyTiles;
+  auto kern = a.drop.thr ? (runs ? lg::fwd_large_kernel<true, true> : lg::fwd_large_kernel<false, true>)
+                         : (runs ? lg::fwd_large_kernel<true, false> : lg::fwd_large_kernel<false, false>);
+  // (before the tensor maps: a thread's first runtime call binds the device's
+  // context, which encoding them needs and does not do)
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, lg::kSmemBytes) !=
       cudaSuccess)
+    return SWIN_ERR_CUDA;
+  if (!lg::tile_maps(&mq, a.q, a.g) || !lg::tile_maps(&mk, a.k, a.g) || !lg::tile_maps(&mv, a.v, a.g))
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, lg::kThreads, lg::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mk, mv);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;

@@ -60,6 +60,9 @@ static_assert(kSmemBytes <= 232448, "over the 227 KB of shared memory a CTA may 
 constexpr int kQWarp = 12, kKWarp = 13, kVWarp = 14;
 constexpr uint32_t kColS = 0, kColdP = 128, kColdQ = 256;
 
+// kDrop: the thread of a query row draws the forward's decisions of each 16-key
+// group again; dP counts where they keep, times the kept values' scale.
+template <bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     bwdq_kernel(const BwdArgs a, const __grid_constant__ TileMaps tmq, const __grid_constant__ TileMaps tmk,
                 const __grid_constant__ TileMaps tmv, const __grid_constant__ TileMaps tmdo) {
@@ -265,6 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool live = false;
     float lse2 = 0.f, dpart = 0.f, delta = 0.f;
     uint32_t bs_phase = 0;
+    KeepDraw draw;
+    if (kDrop) draw.init(a.drop, g.n);
+    uint64_t blk0 = 0;  // generator block of the row's keys in this warpgroup's half of key tile 0
     bool ok = true;
     if (a.debug_force_timeout) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     for (int64_t t = 0; ok && t < ntiles; ++t) {
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         rbase = slot < g.n ? r.rbase : g.T - 1;
         live = src >= 0 && (!a.land || __ldg(a.land + (int64_t)x.b * g.tokens + src) == 0);
         lse2 = live ? __ldg(a.lse + ((int64_t)x.b * g.heads + x.h) * g.tokens + src) * kLog2e : 0.f;
+        if (kDrop) blk0 = draw.row(x.b, x.h, g.heads, g.tokens, src) + 8u * grp;
         dpart = 0.f;
         if (delta_given) delta = live ? __ldcg(a.delta + ((int64_t)x.b * g.heads + x.h) * g.tokens + src) : 0.f;
       }
@@ -307,6 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(tmem + lane_addr + kColS + col + 16, sv1);
         tmem_ld16(tmem + lane_addr + kColdP + col, dv0);
         tmem_ld16(tmem + lane_addr + kColdP + col + 16, dv1);
+        uint32_t keep = 0u;  // the two groups' decisions, at bits 0-3 and 4-7 of the bytes
+        if (kDrop) {
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) keep |= draw.group(blk0 + 16u * kt + 4u * c2 + 2u * k) << (4 * k);
+        }
         tmem_wait_ld_tied(sv0, sv1);
         tmem_tie(dv0, dv1);
 #pragma unroll
@@ -325,7 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float x0 = fmaf(__uint_as_float(sv[e]), cs, b0) - lse2;
             const float x1 = fmaf(__uint_as_float(sv[e + 1]), cs, b1) - lse2;
             const float p0 = live ? ex2(x0) : 0.f, p1 = live ? ex2(x1) : 0.f;
-            const float d0 = __uint_as_float(dv[e]), d1 = __uint_as_float(dv[e + 1]);
+            float d0 = __uint_as_float(dv[e]), d1 = __uint_as_float(dv[e + 1]);
+            if (kDrop) {
+              d0 = keep_bit(keep >> (4 * hh), e) ? d0 * a.drop.scale : 0.f;
+              d1 = keep_bit(keep >> (4 * hh), e + 1) ? d1 * a.drop.scale : 0.f;
+            }
             if (!second) {
               dpart = fmaf(p0, d0, dpart);
               dpart = fmaf(p1, d1, dpart);
@@ -397,10 +413,10 @@ namespace bkv {
 constexpr int kK = 0, kV = kTileBytes, kKm = 2 * kTileBytes;  // resident per item
 constexpr int kStage = kKm + kMaskBytes;                         // one query-tile stage
 constexpr int kQ = 0, kdO = kTileBytes, kQm = 2 * kTileBytes, kLse = kQm + kMaskBytes, kDelta = kLse + 512,
-              kRbase = kDelta + 512;
+              kRbase = kDelta + 512, kSrc = kRbase + 512;
 constexpr int kStageBytes = 70 * 1024;
 constexpr int kMaxBiasRows = 8192;
-static_assert(kStage % 1024 == 0 && kStageBytes % 1024 == 0 && kRbase + 512 <= kStageBytes, "layout");
+static_assert(kStage % 1024 == 0 && kStageBytes % 1024 == 0 && kSrc + 512 <= kStageBytes, "layout");
 // Shared memory with kQS query-tile stages. One stage leaves room for the
 // head's bias column, the dBias accumulator and the diagonal-sum scratch; two
 // stages (a launch with neither bias nor dBias) load the next query tile
@@ -423,7 +439,11 @@ struct Lay {
 constexpr int kKVWarp = 12, kQWarp = 13, kdOWarp = 14;
 constexpr uint32_t kColS = 0, kColdP = 128, kColdV = 256, kColdK = 384;
 
-template <int kQS>
+// kDrop: a generator block holds eight keys of one query, and a thread here is a
+// key: of a warp's 32 keys against 16 queries, each lane draws the 16 keys of
+// half a query's row (two blocks), and the queries' 32-bit words then go round
+// the warp, one shuffle a query.
+template <int kQS, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     bwdkv_kernel(const BwdArgs a, const __grid_constant__ TileMaps tmq, const __grid_constant__ TileMaps tmk,
                  const __grid_constant__ TileMaps tmv, const __grid_constant__ TileMaps tmdo) {
@@ -540,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<float4 *>(sp + kLse + 16 * lane) = make_float4(lse2[0], lse2[1], lse2[2], lse2[3]);
         *reinterpret_cast<float4 *>(sp + kDelta + 16 * lane) = make_float4(dl[0], dl[1], dl[2], dl[3]);
         *reinterpret_cast<int4 *>(sp + kRbase + 16 * lane) = make_int4(q.rbase[0], q.rbase[1], q.rbase[2], q.rbase[3]);
+        if (kDrop) *reinterpret_cast<int4 *>(sp + kSrc + 16 * lane) = make_int4(q.src[0], q.src[1], q.src[2], q.src[3]);
         fence_proxy_async_smem();
       }
       mbar_arrive_warp(bar(bFull + s));
@@ -610,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int acc = 0; acc < 2; ++acc) {  // dV, then dK * hd^-1/2
         const uint32_t col = acc ? kColdK : kColdV;
-        const float mul = acc ? a.scale : 1.f;
+        const float mul = acc ? a.scale : kDrop ? a.drop.scale : 1.f;
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(acc ? a.dk : a.dv) + off);
 #pragma unroll 1
         for (int c = 0; c < 8; c += 2) {
@@ -665,12 +686,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         bacc[r] = 0.f;
       }
     };
+    KeepDraw draw;
+    if (kDrop) draw.init(a.drop, g.n);
+    LItem xi = {};      // the item
+    uint32_t kblk = 0;  // generator block of the warp's first key in its query's row
     if (a.debug_force_timeout) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     for (int64_t t = 0; ok && t < ntiles; ++t) {
       const int qt = (int)(t % nqt);
       const int64_t it = t / nqt;
       if (qt == 0) {
         const LItem x = decode(g, its[it]);
+        if (kDrop) {
+          xi = x;
+          kblk = 16u * x.qt + 4u * q4;
+        }
         if (x.h != cur_h) {
           if (cur_h >= 0) {
             if (!bsync()) break;  // every accumulation and bias read of the previous head is done
@@ -718,6 +747,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int rq = rb[c0 + (lane & 15)];
           const bool diag_sum = want_db && keys_run && __all_sync(0xffffffffu, rq == rb[c0] + (lane & 15));
           uint32_t pk[8], dk8[8];
+          uint32_t word = 0u;  // lane q (and q + 16): which of the warp's 32 keys query c0 + q keeps
+          if (kDrop) {
+            const int src = reinterpret_cast<const int *>(sp + kSrc)[64 * grp + c0 + (lane & 15)];
+            const uint64_t at[2] = {draw.row(xi.b, xi.h, g.heads, g.tokens, src) + kblk + 2u * (lane >> 4),
+                                    draw.row(xi.b, xi.h, g.heads, g.tokens, src) + kblk + 2u * (lane >> 4) + 1u};
+            uint4 r[2];
+            draw.ph.blocks(at, r);
+            const uint32_t half = keep_bits(r[0], a.drop.thr) | keep_bits(r[1], a.drop.thr) << 8;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, half, 16);
+            word = lane < 16 ? half | other << 16 : other | half << 16;
+          }
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
             const int c = c0 + e;  // query column within this warpgroup's half
@@ -727,7 +767,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float b0 = has_bias ? bcol[r2.x - roff] : 0.f, b1 = has_bias ? bcol[r2.y - roff] : 0.f;
             const float p0 = ex2(fmaf(__uint_as_float(sv[e]), cs, b0) - l2.x);
             const float p1 = ex2(fmaf(__uint_as_float(sv[e + 1]), cs, b1) - l2.y);
-            const float ds0 = p0 * (__uint_as_float(dv[e]) - d2.x), ds1 = p1 * (__uint_as_float(dv[e + 1]) - d2.y);
+            float dp0 = __uint_as_float(dv[e]), dp1 = __uint_as_float(dv[e + 1]);
+            bool k0 = true, k1 = true;
+            if (kDrop) {
+              k0 = (__shfl_sync(0xffffffffu, word, e) >> lane) & 1u;
+              k1 = (__shfl_sync(0xffffffffu, word, e + 1) >> lane) & 1u;
+              dp0 = k0 ? dp0 * a.drop.scale : 0.f;
+              dp1 = k1 ? dp1 * a.drop.scale : 0.f;
+            }
+            const float ds0 = p0 * (dp0 - d2.x), ds1 = p1 * (dp1 - d2.y);
             if (diag_sum) {
               diag[lane * 17 + e] = ds0;
               diag[lane * 17 + e + 1] = ds1;
@@ -735,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (ds0 != 0.f) atomicAdd(bacc + (r2.x - roff), ds0);
               if (ds1 != 0.f) atomicAdd(bacc + (r2.y - roff), ds1);
             }
-            pk[e >> 1] = pack_bf16(p0, p1);
+            pk[e >> 1] = pack_bf16(k0 ? p0 : 0.f, k1 ? p1 : 0.f);  // dV takes the kept values' scale at its store
             dk8[e >> 1] = pack_bf16(ds0, ds1);
           }
           if (diag_sum) {
@@ -783,24 +831,28 @@ int large_bwd_max_bias_rows() { return lg::bq::kMaxBiasRows; }
 int launch_bwd_large(const BwdArgs &a, void *stream) {
   if ((a.bias && a.g.T > lg::bq::kMaxBiasRows) || (a.ws && a.g.T > lg::bkv::kMaxBiasRows)) return SWIN_ERR_UNSUPPORTED;
   lg::TileMaps mq, mk, mv, mdo;
-  if (!lg::tile_maps(&mq, a.q, a.g) || !lg::tile_maps(&mk, a.k, a.g) || !lg::tile_maps(&mv, a.v, a.g) ||
-      !lg::tile_maps(&mdo, a.dout, a.g))
-    return SWIN_ERR_CUDA;
   // two query stages in the key-tile kernel when neither the bias column nor
   // the dBias accumulator needs its shared memory
   const bool two = a.bias == nullptr && a.ws == nullptr;
-  auto kv = two ? lg::bkv::bwdkv_kernel<2> : lg::bkv::bwdkv_kernel<1>;
+  auto kv = a.drop.thr ? (two ? lg::bkv::bwdkv_kernel<2, true> : lg::bkv::bwdkv_kernel<1, true>)
+                       : (two ? lg::bkv::bwdkv_kernel<2, false> : lg::bkv::bwdkv_kernel<1, false>);
+  auto kq = a.drop.thr ? lg::bq::bwdq_kernel<true> : lg::bq::bwdq_kernel<false>;
   const int kv_smem = two ? lg::bkv::Lay<2>::kSmemBytes : lg::bkv::Lay<1>::kSmemBytes;
-  if (cudaFuncSetAttribute(lg::bq::bwdq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lg::bq::kSmemBytes) !=
+  // (before the tensor maps: a thread's first runtime call binds the device's
+  // context, which encoding them needs and does not do)
+  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, lg::bq::kSmemBytes) !=
           cudaSuccess ||
       cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, kv_smem) != cudaSuccess)
+    return SWIN_ERR_CUDA;
+  if (!lg::tile_maps(&mq, a.q, a.g) || !lg::tile_maps(&mk, a.k, a.g) || !lg::tile_maps(&mv, a.v, a.g) ||
+      !lg::tile_maps(&mdo, a.dout, a.g))
     return SWIN_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a.o) {
     const int64_t toks = (int64_t)a.g.batch * a.g.tokens;
     lg::delta_kernel<<<(unsigned)((toks + 7) / 8), 256, 0, s>>>(a);
   }
-  lg::bq::bwdq_kernel<<<a.ctas, lg::kThreads, lg::bq::kSmemBytes, s>>>(a, mq, mk, mv, mdo);
+  kq<<<a.ctas, lg::kThreads, lg::bq::kSmemBytes, s>>>(a, mq, mk, mv, mdo);
   kv<<<a.ctas, lg::kThreads, kv_smem, s>>>(a, mq, mk, mv, mdo);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }

@@ -145,6 +145,30 @@ __device__ __forceinline__ uint32_t keep_mask(uint32_t bits, int e) {
 // Key e of a group alone.
 __device__ __forceinline__ bool keep_bit(uint32_t bits, int e) { return (bits & (1u << (8 * (e & 3) + (e >> 2)))) != 0u; }
 
+// The decisions of attention probabilities: row (image b, head h, query token t),
+// key slots in order, ceil(n / 8) blocks a row.
+struct KeepDraw {
+  Philox ph;
+  PairTest test;
+  int nb;
+  __device__ __forceinline__ void init(const Drop &d, int n) {
+    ph.init(d);
+    test.init(d.thr);
+    nb = (n + 7) >> 3;
+  }
+  // first block of a query's row (a pad, token -1: any row will do)
+  __device__ __forceinline__ uint64_t row(int b, int h, int heads, int tokens, int token) const {
+    return (((uint64_t)b * heads + h) * tokens + max(token, 0)) * nb;
+  }
+  // the 16-key group whose first block is b (group_bits)
+  __device__ __forceinline__ uint32_t group(uint64_t b) const {
+    const uint64_t at[2] = {b, b + 1};
+    uint4 r[2];
+    ph.blocks(at, r);
+    return group_bits(r[0], r[1], test);
+  }
+};
+
 // A block's eight decisions, bit e = decision e keeps.
 __device__ __forceinline__ uint32_t keep_bits(const uint4 &u, uint32_t thr) {
   uint32_t m = 0u;

@@ -483,31 +483,6 @@ __device__ __forceinline__ void gather_role(const Geo &g, const StageLayout &lay
   }
 }
 
-// Dropout decisions of a softmax thread's half row (its warpgroup's keys), one
-// 16-key group (two generator blocks) at a time.
-struct KeepDraw {
-  Philox ph;
-  PairTest test;
-  int nb, first;  // generator blocks of a row's keys; the half row's first
-  __device__ __forceinline__ void init(const Geo &g, const Drop &d, int first_block) {
-    ph.init(d);
-    test.init(d.thr);
-    nb = (g.n + 7) >> 3;
-    first = first_block;
-  }
-  // the half row's first block, of the row of query token src (negative: a pad, any row will do)
-  __device__ __forceinline__ uint64_t block(const Geo &g, const ItemCursor &x, int src) const {
-    return (((uint64_t)x.b * g.heads + x.h) * g.tokens + max(src, 0)) * nb + first;
-  }
-  // the group whose first block is b (group_bits)
-  __device__ __forceinline__ uint32_t group(uint64_t b) const {
-    const uint64_t at[2] = {b, b + 1};
-    uint4 r[2];
-    ph.blocks(at, r);
-    return group_bits(r[0], r[1], test);
-  }
-};
-
 // ---------------------------------------------------------------- forward ---
 namespace fwd {
 
@@ -825,7 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t bs_phase = 0;
     float *bvec = reinterpret_cast<float *>(smem + kBvec);
     KeepDraw draw;
-    if (kDrop) draw.init(g, a.drop, kPack == 2 ? 0 : 2 * gb);
+    if (kDrop) draw.init(a.drop, g.n);
+    const int kb0 = kPack == 2 ? 0 : 2 * gb;  // block of the half row's first key
     bool ok = true;
     if (a.debug_force_timeout && grp == 0) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     ItemCursor x;
@@ -863,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kDrop) {       // (the stage is held until P is written)
         const int s = (int)(it % kStages);
         if (!mbar_wait_warp(bar(bFull + s), (uint32_t)(it / kStages) & 1u, ctl)) break;
-        blk = draw.block(g, x, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i]);
+        blk = draw.row(x.b, x.h, g.heads, g.tokens, reinterpret_cast<const int *>(smem + s * kStageBytes + kMeta)[i]) + kb0;
       }
       if (!mbar_wait_warp(bar(bSFull + wb), (uint32_t)(it >> 1) & 1u, ctl)) break;
       tc_fence_after();
@@ -1270,7 +1246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int h_last = count > 0 ? decode_item(g, R - 1).h : 0;  // heads rise by one along the range
     uint32_t wsync_phase = 0;
     KeepDraw draw;
-    if (kDrop) draw.init(g, a.drop, kPack == 2 ? 0 : 2 * gb);
+    if (kDrop) draw.init(a.drop, g.n);
+    const int kb0 = kPack == 2 ? 0 : 2 * gb;  // block of the half row's first key
     bool ok = true;
     if (a.debug_force_timeout) ok = mbar_wait_warp(bar(bNever), 0, ctl);
     // Fold the slot-pair dBias accumulator into bias rows (fixed order) and
@@ -1353,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lse2 = reinterpret_cast<const float *>(sp + kMeta + 512)[i];
       const bool live = (sp + kMeta + 1024)[i] != 0;
       uint64_t blk = 0;  // this half row's first generator block
-      if (kDrop) blk = draw.block(g, x, reinterpret_cast<const int *>(sp + kMeta)[i]);
+      if (kDrop)
+        blk = draw.row(x.b, x.h, g.heads, g.tokens, reinterpret_cast<const int *>(sp + kMeta)[i]) + kb0;
       // pass 1: P = exp2(S*cs + bias2 - lse2); partial delta = sum_j P dP over
       // this half; P (fp32) back over S in TMEM, P (bf16) to the smem tile.
       float delta = 0.f;
@@ -1569,23 +1547,25 @@ bool tensor_maps(TmaSet *t, const void *base, const Geo &g) {
 
 int launch_fwd_tc(const FwdArgs &a, void *stream) {
   TmaSet mq, mk, mv;
-  if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g)) return SWIN_ERR_CUDA;
   auto kern = a.drop.thr ? (a.g.pack == 2 ? fwd::fwd_tc_kernel<2, true> : fwd::fwd_tc_kernel<1, true>)
                          : (a.g.pack == 2 ? fwd::fwd_tc_kernel<2, false> : fwd::fwd_tc_kernel<1, false>);
+  // (before the tensor maps: a thread's first runtime call binds the device's
+  // context, which encoding them needs and does not do)
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, fwd::kSmemBytes) != cudaSuccess)
     return SWIN_ERR_CUDA;
+  if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g)) return SWIN_ERR_CUDA;
   kern<<<a.ctas, fwd::kThreads, fwd::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mk, mv);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }
 
 int launch_bwd_tc(const BwdArgs &a, void *stream) {
   TmaSet mq, mk, mv, mdo;
-  if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g) ||
-      !tensor_maps(&mdo, a.dout, a.g))
-    return SWIN_ERR_CUDA;
   auto kern = a.drop.thr ? (a.g.pack == 2 ? bwd::bwd_tc_kernel<2, true> : bwd::bwd_tc_kernel<1, true>)
                          : (a.g.pack == 2 ? bwd::bwd_tc_kernel<2, false> : bwd::bwd_tc_kernel<1, false>);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd::kSmemBytes) != cudaSuccess)
+    return SWIN_ERR_CUDA;
+  if (!tensor_maps(&mq, a.q, a.g) || !tensor_maps(&mk, a.k, a.g) || !tensor_maps(&mv, a.v, a.g) ||
+      !tensor_maps(&mdo, a.dout, a.g))
     return SWIN_ERR_CUDA;
   kern<<<a.ctas, bwd::kThreads, bwd::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(a, mq, mk, mv, mdo);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;

@@ -31,7 +31,19 @@ CASES = [
 ]
 
 
-def run(case, rate, site=6, seed_index=700, want_bias=True):
+# head_dim 128, windows of any size: one partial key tile, two tiles, a partial second one, ragged 3-D with land,
+# more than one image, windows above 2 048 slots (without a bias: two query stages), 32 key tiles (slots in runs)
+LARGE = [
+    ((21, 45), (8, 12), (4, 6), (0, 1), 2, 128, 2, "bf16", None),
+    ((32, 40), (16, 16), (8, 8), (0, 1), 2, 128, 1, "bf16", (0.3, 0.3)),
+    ((14, 27), (12, 12), (6, 6), (1, 0), 1, 128, 2, "bf16", None),
+    ((3, 40, 70), (2, 16, 16), (1, 8, 8), (0, 0, 1), 1, 128, 1, "bf16", (0.2, 0.5)),
+    ((60, 100), (30, 100), (15, 50), (0, 1), 1, 128, 1, "bf16", None),
+    ((64, 72), (64, 64), (32, 32), (0, 1), 1, 128, 1, "bf16", None),
+]
+
+
+def run(case, rate, site=6, seed_index=700, want_bias=True, give_o=False):
     from shifted_window_attention_cyclic_gb300 import swin_attn as C
     from shifted_window_attention_cyclic_gb300.dropout import Dropout, DropoutState
     from shifted_window_attention_cyclic_gb300.functional import SwinWindowAttention
@@ -43,7 +55,8 @@ def run(case, rate, site=6, seed_index=700, want_bias=True):
     bias = t["bias"] if want_bias else None
     drop = Dropout(DropoutState(2**64 - 3, 9), rate, site)
     o, lse = attn.forward(t["q"], t["k"], t["v"], bias, t["land"], dropout=drop)
-    dq, dk, dv, dbias = attn.backward(t["q"], t["k"], t["v"], t["dout"], lse, bias, t["land"], o=o, dropout=drop)
+    dq, dk, dv, dbias = attn.backward(t["q"], t["k"], t["v"], t["dout"], lse, bias, t["land"], dropout=drop,
+                                      o=o if give_o else None, want_dbias=want_bias or hd != 128)
     torch.cuda.synchronize()
     assert C.swin_attn_status(attn.plan) == 0
     got = dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv, dbias=dbias)
@@ -51,8 +64,12 @@ def run(case, rate, site=6, seed_index=700, want_bias=True):
     flat = lambda n: torch.from_numpy(x[n]).double().reshape(batch, -1, heads * hd)  # noqa: E731
     land = None if x["land"] is None else torch.from_numpy(x["land"]).reshape(batch, -1) != 0
     b64 = torch.from_numpy(x["bias"]).double()
-    want = ref.attn(flat("q"), flat("k"), flat("v"), b64 if want_bias else 0 * b64, land,
-                    (tables[0], tables[1], tables[3]), heads, (2**64 - 3, 9, site, rate), flat("dout"))
+    rel = tables[3]
+    if rel is None:  # a plan keeps the slot pairs' bias rows up to 2 048 slots; without a bias any row will do
+        assert not want_bias
+        rel = np.zeros((tables[0].shape[1],) * 2, np.int64)
+    want = ref.attn(flat("q"), flat("k"), flat("v"), b64 if want_bias else 0 * b64, land, (tables[0], tables[1], rel), heads,
+                    (2**64 - 3, 9, site, rate), flat("dout"))
     return attn, t, got, want
 
 
@@ -75,7 +92,32 @@ def test_parity(case, rate):
     assert (lse[~sea] == -np.inf).all() and np.abs(lse[sea] - want["lse"].numpy()[sea]).max(initial=0) <= 1e-4
 
 
-@pytest.mark.parametrize("case", [CASES[0], CASES[4], CASES[7]], ids=["simt", "one_window", "two_windows"])
+@pytest.mark.parametrize("give_o", [False, True], ids=["delta_summed", "delta_from_o"])
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: "x".join(map(str, c[0])))
+def test_parity_large(case, give_o):
+    n = int(np.prod(case[1]))
+    want_bias = n <= 2048
+    rate = 0.3 if give_o else 0.1
+    _, _, got, want = run(case, rate, want_bias=want_bias, give_o=give_o)
+    c = ref.kept_scale(rate)
+    for name in ("o", "dq", "dk", "dv") + (("dbias",) if want_bias and not give_o else ()):
+        max_abs, rel = errors(host(got[name]).reshape(want[name].shape), want[name].numpy())
+        assert max_abs <= BF16_MAX_ABS * c and rel <= BF16_REL_L2, (name, max_abs, rel)
+    if want_bias and give_o:
+        # delta = dO . O carries O's rounding, half a step of 2^-8 |O|: a row's dS is off by P times
+        # sum_c |dO_c| 2^-9 |O_c| at most, and a bias row adds up its pairs' errors
+        d = torch.from_numpy(workloads.generate(workloads.custom(*case[:9], seed_index=700))["dout"]).double()
+        heads = case[4]
+        slack = (d.reshape(case[6], -1, heads, 128).abs() * want["o"].view(case[6], -1, heads, 128).abs()).sum(-1) * 2.0**-8
+        assert np.abs(host(got["dbias"]) - want["dbias"].numpy()).max() <= BF16_MAX_ABS * c + float(slack.sum((0, 1)).max())
+    lse = host(got["lse"]).reshape(want["lse"].shape)
+    sea = np.isfinite(want["lse"].numpy())
+    # the bar of the large windows' log-sum-exp (lazy rescaling sums P in another order)
+    assert (lse[~sea] == -np.inf).all() and np.abs(lse[sea] - want["lse"].numpy()[sea]).max(initial=0) <= 2e-3
+
+
+@pytest.mark.parametrize("case", [CASES[0], CASES[4], CASES[7], LARGE[2]],
+                         ids=["simt", "one_window", "two_windows", "large"])
 def test_every_key_of_a_row_dropped(case):
     """At a rate of 65535/65536 nearly every decision drops: O is 0 there, not NaN, and what is kept is scaled by 65536."""
     _, _, got, want = run(case, 65535 / 65536)
@@ -129,19 +171,13 @@ def test_captured_replay_takes_the_step_of_the_state():
 
 
 def test_refusals():
-    from shifted_window_attention_cyclic_gb300 import swin_attn as C
     from shifted_window_attention_cyclic_gb300.dropout import Dropout, DropoutState
     from shifted_window_attention_cyclic_gb300.functional import SwinWindowAttention
-    big = SwinWindowAttention((16, 16), (16, 16), (8, 8), (0, 1), 1, 128)
-    q = torch.zeros(big.shape, device="cuda", dtype=torch.bfloat16)
-    drop = Dropout(DropoutState(1), 0.1, 0)
-    with pytest.raises(C.SwinAttnError, match="unsupported"):
-        big.forward(q, q, q, dropout=drop)
-    lse = torch.zeros(big.lse_shape, device="cuda")
-    with pytest.raises(C.SwinAttnError, match="unsupported"):
-        big.backward(q, q, q, q, lse, dropout=drop)
-    big.forward(q, q, q, dropout=Dropout(drop.state, 0.0, 0))
+    attn = SwinWindowAttention((16, 16), (16, 16), (8, 8), (0, 1), 1, 128)
+    q = torch.zeros(attn.shape, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="Dropout"):
-        big.forward(q, q, q, dropout=0.1)
+        attn.forward(q, q, q, dropout=0.1)
     with pytest.raises(ValueError, match="its state"):
-        big.forward(q, q, q, dropout=Dropout(DropoutState(1, device="cpu"), 0.1, 0))
+        attn.forward(q, q, q, dropout=Dropout(DropoutState(1, device="cpu"), 0.1, 0))
+    with pytest.raises(ValueError, match="dtype"):
+        attn.forward(q.float(), q, q, dropout=Dropout(DropoutState(1), 0.1, 0))
