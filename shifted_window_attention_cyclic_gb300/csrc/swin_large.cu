@@ -109,8 +109,9 @@ __device__ __forceinline__ LItem decode_pair(const Geo &g, int64_t it) {
 // kRuns: key/value tiles load runs of slots as boxes (windows of at least
 // kRunMinKeyTiles key tiles); otherwise every row by gather4.
 // kDrop: dropout of the probabilities. A softmax thread draws its row's decisions
-// for 64 keys at a time (four groups in a rolled loop) and ANDs them onto packed
-// P; the row sums are taken before, and the kept values' scale goes into 1 / l.
+// and ANDs them onto packed P, one 16-key group a trip of its second pass (short
+// code: see the small-window forward); the row sums are taken before, and the
+// kept values' scale goes into 1 / l.
 template <bool kRuns, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_large_kernel(const FwdArgs a, const __grid_constant__ TileMaps tmq, const __grid_constant__ TileMaps tmk,
@@ -432,21 +433,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // pass 2: x = S*cs + bias2, P = exp2(x - m) over S, row sum
       const float msub = any ? m_run : 0.f;
       float2 sp2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      constexpr int kG = kDrop ? 1 : 4;  // 16-key groups a trip
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t sv[4][16];
+      for (int c = 0; c < 8 / kG; ++c) {
+        uint32_t sv[kG][16];
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) tmem_ld16(tS + 64u * c + 16u * k4, sv[k4]);
-        tmem_wait_ld_tied(sv[0], sv[1]);
-        tmem_wait_ld_tied(sv[2], sv[3]);
+        for (int k4 = 0; k4 < kG; ++k4) tmem_ld16(tS + 16u * (kG * c + k4), sv[k4]);
+        uint32_t keep = 0u;
+        if constexpr (kDrop) {
+          keep = draw.group(blk0 + 16u * kt + 2u * c);
+          tmem_wait_ld_tied(sv[0]);
+        } else {
+          tmem_wait_ld_tied(sv[0], sv[1]);
+          tmem_wait_ld_tied(sv[2], sv[3]);
+        }
         // x - m = S*cs + (bias2 - m) for the 64 keys, in place: the shared-memory
         // bias reads run back to back (no TMEM store between them)
         const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-msub, -msub);
         if (has_bias) {
           const uint32_t brow = bcol_u32 + 4u * (uint32_t)rbase;  // this row's end of the column
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
-            const int v = roff[64 * c + 16 * k4];  // the same entry for every lane
+          for (int k4 = 0; k4 < kG; ++k4) {
+            const int v = roff[16 * (kG * c + k4)];  // the same entry for every lane
             if (v & 1) {
               // regular chunk: key e's value sits 4e bytes below the first key's
               float bv[16];
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const uint2 w = *reinterpret_cast<const uint2 *>(roff + 64 * c + 16 * k4 + e);
+              const uint2 w = *reinterpret_cast<const uint2 *>(roff + 16 * (kG * c + k4) + e);
               const int4 r4 = make_int4((int)(int16_t)(w.x & 0xFFFFu), (int)w.x >> 16, (int)(int16_t)(w.y & 0xFFFFu),
                                         (int)w.y >> 16);
               const float2 b01 = make_float2(lds_f32(brow + r4.x), lds_f32(brow + r4.y));
@@ -482,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int k4 = 0; k4 < 4; ++k4) {
+          for (int k4 = 0; k4 < kG; ++k4) {
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               const float2 x =
@@ -492,18 +500,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        uint32_t keep[2] = {0u, 0u};  // groups 0-1, 2-3 of the 64 keys, at bits 0-3 and 4-7 of the bytes
-        if (kDrop) {
-          uint64_t b = blk0 + 16u * kt + 8u * c;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k, b += 2) {
-            const uint32_t bits = draw.group(b) << (4 * (k & 1));
-            if (k < 2) keep[0] |= bits; else keep[1] |= bits;
-          }
-        }
         // P = exp2(x - m) in bf16 over S, row sum
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
+        for (int k4 = 0; k4 < kG; ++k4) {
           uint32_t pv[8];
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
@@ -511,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : make_float2(0.f, 0.f);
             sp2[(e >> 1) & 1] = __fadd2_rn(sp2[(e >> 1) & 1], p);
             pv[e >> 1] = pack_bf16(p.x, p.y);
-            if (kDrop) pv[e >> 1] &= keep_mask(keep[k4 >> 1] >> (4 * (k4 & 1)), e);
+            if (kDrop) pv[e >> 1] &= keep_mask(keep, e);
           }
-          tmem_st8(tS + 64u * c + 16u * k4, pv);
+          tmem_st8(tS + 16u * (kG * c + k4), pv);
         }
       }
       const float2 sum2 = __fadd2_rn(sp2[0], sp2[1]);
