@@ -290,7 +290,7 @@ typedef struct {
 } swin_attn_norm;
 
 typedef struct {
-  int64_t images, tokens; /* >= 0; images * tokens < 2^31 */
+  int64_t images, tokens; /* >= 0; images * tokens < 2^31 (else UNSUPPORTED) */
   int32_t channels;       /* a multiple of 8, up to 8192 (else UNSUPPORTED) */
   int32_t dtype;          /* SWIN_F32 or SWIN_BF16: the activations' type */
 } swin_attn_rows;

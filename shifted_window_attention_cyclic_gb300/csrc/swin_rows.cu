@@ -890,7 +890,10 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
     const int64_t i0 = v * 8;
     uint4 bits = make_uint4(0u, 0u, 0u, 0u);
     if (kMode == 0) bits = ph.block((uint64_t)v);
-    if (kMode == 1 && keep_one(ph, (uint64_t)(i0 / span), d.thr)) bits = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (kMode == 1) {  // (32-bit division: a quarter of the long one's work)
+      const uint64_t i = nvec <= UINT32_MAX ? (uint32_t)v / (uint32_t)min(span >> 3, (int64_t)UINT32_MAX) : v / (span >> 3);
+      if (keep_one(ph, i, d.thr)) bits = make_uint4(~0u, ~0u, ~0u, ~0u);
+    }
     if (i0 + 8 <= n) {
       Raw<T> in;
       load8(x + i0, in, wide);
@@ -1161,6 +1164,8 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   a.C = r->channels;
   a.images = (int)r->images;
   a.tokens = branch ? r->tokens : a.rows;  // the norm alone does not look at images
+  const int64_t groups = a.gate && want_post ? image_groups(a.images) : 1;
+  if (groups > 65535) return SWIN_ERR_UNSUPPORTED;  // (a grid's y)
   const Split sp = split_rows(a.rows, a.C, sms, true, true);
   a.chunk = sp.chunk;
   if (want_pre || want_post) {
@@ -1201,8 +1206,6 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
     c.dgate = g.gate;
   }
   const int tiles = (a.C + 31) / 32;
-  const int64_t groups = a.gate && want_post ? image_groups(a.images) : 1;
-  if (groups > 65535) return SWIN_ERR_UNSUPPORTED;
   if (groups > 1) c.groups = a.part_post + join_slots(sp.ctas, a.images) * 2 * a.C;
   if ((rc = launch_columns(c, tiles, (unsigned)groups, st))) return rc;
   if (groups > 1) {  // the groups' sums are what a join without a gate would have left

@@ -9,9 +9,8 @@ backward is done.
 """
 from __future__ import annotations
 
-import ctypes
-
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import swin_attn as C
 
@@ -26,7 +25,12 @@ class DropoutState:
         if not 0 <= int(seed) < 2 ** 64:
             raise ValueError("seed: a whole number of 64 bits, got %r" % (seed,))
         seed = int(seed) - (2 ** 64 if int(seed) >= 2 ** 63 else 0)
-        self.tensor = torch.tensor([seed, int(step)], dtype=torch.int64, device=device)
+        self._tensor = torch.tensor([seed, int(step)], dtype=torch.int64, device=device)
+
+    @property
+    def tensor(self):
+        """The state itself (write into it to restore a saved one; dropouts keep its address)."""
+        return self._tensor
 
     def advance(self, steps=1):
         """Go on to the next training step (on the current stream; may be
@@ -118,6 +122,7 @@ class _DropoutFn(torch.autograd.Function):
         return apply_dropout(x.contiguous(), drop, span)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         ctx.saved_tensors
         return apply_dropout(dy.contiguous(), ctx.drop, ctx.span), None, None

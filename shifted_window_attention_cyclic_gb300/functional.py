@@ -214,14 +214,17 @@ class SwinBlockPair:
         self.swmsa = SwinWindowAttention(grid, window, shift, periodic, heads, head_dim, batch, dtype, has_land,
                                          impl, device)
 
-    def forward(self, first, second, land=None):
-        """first, second: (q, k, v, bias) of the W-MSA and the SW-MSA layer.
+    def forward(self, first, second, land=None, dropout=(None, None)):
+        """first, second: (q, k, v, bias) of the W-MSA and the SW-MSA layer;
+        dropout: the layers' Dropouts (sites of their own).
         Returns ((O, lse) of the first, (O, lse) of the second)."""
-        return self.wmsa.forward(*first, land=land), self.swmsa.forward(*second, land=land)
+        return (self.wmsa.forward(*first, land=land, dropout=dropout[0]),
+                self.swmsa.forward(*second, land=land, dropout=dropout[1]))
 
-    def backward(self, first, second, dout_first, dout_second, lse_first, lse_second, land=None):
+    def backward(self, first, second, dout_first, dout_second, lse_first, lse_second, land=None,
+                 dropout=(None, None)):
         """Gradients (dq, dk, dv, dbias) of both layers, second layer first
-        (the order a training step runs them)."""
-        g2 = self.swmsa.backward(*second[:3], dout_second, lse_second, second[3], land)
-        g1 = self.wmsa.backward(*first[:3], dout_first, lse_first, first[3], land)
+        (the order a training step runs them); dropout as in forward."""
+        g2 = self.swmsa.backward(*second[:3], dout_second, lse_second, second[3], land, dropout=dropout[1])
+        g1 = self.wmsa.backward(*first[:3], dout_first, lse_first, first[3], land, dropout=dropout[0])
         return g1, g2

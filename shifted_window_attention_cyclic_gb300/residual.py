@@ -15,6 +15,7 @@ import math
 from collections import namedtuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import swin_attn as C
 from .dropout import check_dropout, on, same_rows
@@ -211,6 +212,7 @@ class _NormFn(torch.autograd.Function):
         return norm.forward(x, gamma, beta)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         x, gamma, beta = ctx.saved_tensors
         want = any(ctx.needs_input_grad[2:])
@@ -236,6 +238,7 @@ class _JoinFn(torch.autograd.Function):
         return (y, h) if h is not None else (y, None)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         y, z, *params = ctx.saved_tensors[:8]
         if dy is None and dh is None:

@@ -130,6 +130,44 @@ def test_every_key_of_a_row_dropped(case):
             assert (g[w == 0] == 0).all()
 
 
+def test_simt_and_tensor_core_kernels_drop_the_same():
+    """One plan geometry on both kernel families (bf16, head_dim 32): the same keys are dropped, so V = one-hot rows
+    read the same zeros out of P."""
+    from shifted_window_attention_cyclic_gb300.dropout import Dropout, DropoutState
+    from shifted_window_attention_cyclic_gb300.functional import SwinWindowAttention
+    drop = Dropout(DropoutState(41), 0.4, 2)
+    got = []
+    for impl in ("simt", "tc"):
+        attn = SwinWindowAttention((8, 12), (4, 8), (2, 4), (0, 1), 2, 32, 2, "bf16", impl=impl)
+        gen = torch.Generator().manual_seed(1)
+        q, k = (torch.randn(attn.shape, generator=gen).bfloat16().cuda() for _ in range(2))
+        # token (r, c) has a one in channel 8 (r % 4) + c % 8: another channel for every token of a window
+        ch = 8 * (torch.arange(8)[:, None] % 4) + torch.arange(12) % 8
+        v = torch.nn.functional.one_hot(ch, 32).bfloat16()[None, :, :, None].expand(2, 8, 12, 2, 32)
+        got.append(attn.forward(q, k, v.reshape(attn.shape).contiguous().cuda(), dropout=drop)[0])
+    assert torch.equal(got[0] == 0, got[1] == 0) and 0.3 < (got[0] == 0).float().mean() < 0.95
+    assert (got[0].float() - got[1].float()).abs().max() <= BF16_MAX_ABS * ref.kept_scale(0.4)
+
+
+def test_block_pair_takes_a_dropout_for_each_layer():
+    from shifted_window_attention_cyclic_gb300.dropout import Dropout, DropoutState
+    from shifted_window_attention_cyclic_gb300.functional import SwinBlockPair
+    pair = SwinBlockPair((16, 24), (4, 8), (0, 1), 2, 32)
+    layers = [tuple(torch.randn(pair.wmsa.shape, device="cuda").bfloat16() for _ in range(3)) + (pair.wmsa.new_bias(),)
+              for _ in range(2)]
+    dout = torch.randn(pair.wmsa.shape, device="cuda").bfloat16()
+    state = DropoutState(4)
+    drops = Dropout(state, 0.2, 0), Dropout(state, 0.2, 1)
+    (o1, l1), (o2, l2) = pair.forward(*layers, dropout=drops)
+    g1, g2 = pair.backward(*layers, dout, dout, l1, l2, dropout=drops)
+    for attn, layer, drop, o, lse, g in ((pair.wmsa, layers[0], drops[0], o1, l1, g1),
+                                         (pair.swmsa, layers[1], drops[1], o2, l2, g2)):
+        assert torch.equal(attn.forward(*layer, dropout=drop)[0], o)
+        want = attn.backward(*layer[:3], dout, lse, layer[3], dropout=drop)
+        assert all(torch.equal(a, b) for a, b in zip(want, g))
+    assert not torch.equal(o1, pair.forward(*layers)[0][0])
+
+
 def test_rate_zero_is_the_attention_without_dropout():
     for case in (CASES[0], CASES[4]):
         attn, t, got, _ = run(case, 2.0**-18)  # rounds to T = 0

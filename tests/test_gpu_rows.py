@@ -406,6 +406,12 @@ def test_a_block_trains_through_all_of_them():
         assert e <= 5 * OPS, (n, float(e))
     assert (y.double().cpu().view(y64.shape) - y64).norm() <= 5 * OPS * y64.norm()
 
+    # second derivatives are refused, not wrong
+    x = torch.randn(1, 3, 64, device="cuda", requires_grad=True)
+    g, = torch.autograd.grad(block_norm(BlockNorm(64, dtype="f32"), x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable|does not require grad"):
+        g.sum().backward()
+
     # a state advanced between the forward and the backward is an error, not a wrong gradient
     out = dropout(p["x"], drops[0])
     state.advance()
