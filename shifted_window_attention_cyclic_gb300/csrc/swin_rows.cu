@@ -266,6 +266,15 @@ struct Shape {
   static_assert(smem <= 227 * 1024, "over a CTA's shared memory");
 };
 
+// The decisions of a thread's vectors of a row, one generator block each.
+template <int NV>
+__device__ __forceinline__ void draw_row(const Philox &ph, uint64_t vec, int step, uint4 (&bits)[NV]) {
+  uint64_t at[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) at[j] = vec + (uint64_t)(j * step);
+  ph.blocks(at, bits);
+}
+
 // ---- sums over a row ---------------------------------------------------------
 // Sum of a float, or of a pair, over the TPR threads of a row. Rows of up to 32
 // threads stay inside a warp; wider rows are the whole CTA and exchange one
@@ -602,6 +611,8 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
       ring.before_fetch();
       fetch(in);
       in = R::next(in);
+      uint4 bits[NV];  // drawn together here, where no row waits for them yet (1-degree: 87 us, 89 us at their use)
+      if (kBranch && a.drop.thr) draw_row(ph, vec, TPR, bits);
       ring.template arrived<D>();
       const bool live = row < count;
       // both rows' statistics, in two rounds of sums
@@ -699,12 +710,11 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
               for (int e = 0; e < 4; ++e) z[j][e] = mul(z[j][e], both(z_rstd));
             }
             if (a.drop.thr) {
-              const uint4 bits = ph.block((uint64_t)(vec + j * TPR));
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                g[j][e] = kept(bits, e, a.drop.thr, g[j][e]);
+                g[j][e] = kept(bits[j], e, a.drop.thr, g[j][e]);
                 // what was dropped takes no part, were it infinite (a row's norm has it in its statistics anyway)
-                if (!post) z[j][e] = kept(bits, e, a.drop.thr, z[j][e]);
+                if (!post) z[j][e] = kept(bits[j], e, a.drop.thr, z[j][e]);
               }
             }
 #pragma unroll
