@@ -533,7 +533,10 @@ constexpr uint32_t kTmemCols = 512, kColS = 0, kColO = 256;
 // that the one-window kernel carries no code for the second window.
 // kDrop: dropout of the probabilities. A softmax thread draws its row's decisions
 // beside the exponentials and ANDs them onto packed P; the row sums are taken
-// before, and the kept values' scale goes into the epilogue's 1 / l.
+// before, and the kept values' scale goes into the epilogue's 1 / l. (Drawn by the
+// epilogue warps, one bit per key through shared memory, the 256 x 540 stage took
+// 351 us: those warps have no idle time. By four more warps, the registers split
+// over the roles, 519 us.)
 template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_tc_kernel(const FwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
@@ -859,12 +862,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 sp2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if constexpr (kDrop) {
         // The same arithmetic in two rolled passes of one 16-key group a trip, x
-        // going back over S in between: all roles' code together outgrows the
-        // instruction caches, and with the generator's in it the unrolled form
-        // below took 351 us on the 256 x 540 stage (16 heads, 96 slots) with the
-        // decisions drawn ahead, 348 us drawn beside the exponentials; this one
-        // 289 us (two groups a trip 345 us; without dropout 216 us, 210 us in
-        // this form, which is 3 % slower on 128-slot windows).
+        // going back over S in between. Short code is what counts here (all roles
+        // run at once on every scheduler, and 0.4 to 0.7 cycles an issue are spent
+        // waiting for instructions): on the 256 x 540 stage (16 heads, 96 slots)
+        // the unrolled form below took 351 us with the decisions drawn ahead and
+        // 348 us with them beside the exponentials, two groups a trip 345 us, this
+        // form 289 us. Without dropout that stage takes 216 us, and 210 us in this
+        // form, which is 3 % slower on 128-slot windows: those keep the other.
         uint32_t sv[16];
 #pragma unroll 1
         for (int gi = gb; gi < ge; ++gi) {
@@ -1023,7 +1027,9 @@ __device__ __forceinline__ uint32_t pds_chunk(int i, int c) {
 // dP is zeroed where it lies in TMEM (pass 2 then needs no decisions) and its P
 // in the dV operand. The kept values' scale c is left out of both passes
 // (dS / c = P (keep dP - sum P keep dP)) and taken by the epilogue's multiplier
-// of dV, dK and dQ and by the dBias fold.
+// of dV, dK and dQ and by the dBias fold. 256 x 540 stage: 560 us, 447 us without
+// dropout; of the difference 60 us are the use of the decisions, the rest the
+// generator (ALU 45 %, wide multiplies 36 % of their pipes, tensor pipe 9 %).
 template <int kPack, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_tc_kernel(const BwdArgs a, const __grid_constant__ TmaSet tmq, const __grid_constant__ TmaSet tmk,
