@@ -55,7 +55,8 @@ def param(gen, shape, std, mean, present=True):
     return t.cuda(), t.double()
 
 
-WIDTHS = [8, 24, 32, 40, 64, 96, 128, 200, 256, 264, 384, 512, 520, 1024, 1032, 2048, 2056, 4096, 4104, 8192]
+WIDTHS = [8, 24, 32, 40, 64, 72, 96, 128, 136, 184, 200, 256, 264, 384, 392, 512, 520, 768, 1024, 1032, 1536, 2048, 2056,
+          2320, 4096, 4104, 5000, 8192]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -116,7 +117,7 @@ PRESENT = [ALL, (), ("scale", "pre_gamma"), ("gate", "post_gamma"), ("post_beta"
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("post,pre", JOINS)
-@pytest.mark.parametrize("channels", [8, 96, 256, 512, 648, 1024, 1600, 2056, 8192])
+@pytest.mark.parametrize("channels", [8, 56, 96, 168, 256, 376, 512, 648, 1024, 1600, 2056, 5128, 8192])
 def test_join(channels, post, pre, dtype):
     from shifted_window_attention_cyclic_gb300.residual import ResidualJoin
     join = ResidualJoin(channels, post, pre, 1e-5, dtype)
@@ -169,7 +170,7 @@ def test_dropout(n, dtype):
     gen = torch.Generator().manual_seed(n)
     x, x64 = make(gen, (n,), dtype)
     state = DropoutState(2**63 + n, 2**32 + 5)  # the step counts modulo 2^32
-    for rate, span in ((0.1, 1), (0.5, 8), (0.3, 24), (65535 / 65536, 1), (0.25, 3), (0.4, 10**6)):
+    for rate, span in ((0.1, 1), (0.5, 8), (0.3, 24), (65535 / 65536, 1), (0.25, 3), (0.4, 10**6), (0.3, 2), (0.3, 7), (0.3, 9), (0.2, 1001)):
         for site in (0, 2**32 - 1):
             got = apply_dropout(x, Dropout(state, rate, site), span).double().cpu()
             keep = torch.from_numpy(ref.keep(np.arange(n) // span, 2**63 + n, 5, site, rate))
