@@ -5,6 +5,8 @@ single calls into the CUDA library (swin_attn_fwd, swin_attn_bwd).
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import torch
 
 from . import swin_attn as C
@@ -19,6 +21,9 @@ def check_tensor(name, t, shape, dtype, device):
     reads and writes every tensor through a raw pointer and cannot check any
     of this itself; a wrong shape or dtype would read or write past the
     caller's buffers."""
+    if (isinstance(t, torch.Tensor) and t.device == device and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous() and not t.data_ptr() % 16):
+        return  # as a rule: what follows says which
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s: expected a torch.Tensor, got %s" % (name, type(t).__name__))
     if t.device != device:
@@ -133,8 +138,9 @@ class SwinWindowAttention:
             dbias = torch.empty(self.bias_shape, dtype=torch.float32, device=self.device)  # overwritten
         if drop is not None:
             # a workspace of the call's own, on its stream: calls and captured graphs may overlap
-            with torch.cuda.stream(stream):
-                ws = torch.empty(max(C.swin_attn_workspace_bytes(self.plan), 256), dtype=torch.uint8, device=self.device)
+            nbytes = max(C.swin_attn_workspace_bytes(self.plan), 256)
+            with torch.cuda.stream(stream) if stream is not None else nullcontext():
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         else:
             ws = self.workspace()  # dBias partial tables; for head_dim 128 also delta
         if drop is not None:

@@ -301,22 +301,17 @@ def swin_attn_bwd_o(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, d
 
 
 def swin_attn_fwd_dropout(plan: Plan, q, k, v, bias, land, o, lse, drop: swin_attn_drop, stream=None) -> None:
-    pq, pk, pv, po, plse = _acts(("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse))
-    _check(load_library().swin_attn_fwd_dropout(plan.handle, pq, pk, pv, _ptr(bias, 4, "bias"),
-                                                _ptr(land, 4, "land"), po, plse, drop, _handle(stream)),
-           "swin_attn_fwd_dropout")
+    _check(load_library().swin_attn_fwd_dropout(plan.handle, *map(_addr, (q, k, v, bias, land, o, lse)), drop,
+                                                _handle(stream)), "swin_attn_fwd_dropout")
 
 
 def swin_attn_bwd_dropout(plan: Plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace,
                           drop: swin_attn_drop, stream=None) -> None:
     """Backward with the forward's dropout (the same site, rate and an unchanged state)."""
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    pq, pk, pv, po, pdo, plse, pdq, pdk, pdv = _acts(("q", q), ("k", k), ("v", v), ("o", o), ("dout", dout),
-                                                     ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv))
-    _check(load_library().swin_attn_bwd_dropout(plan.handle, pq, pk, pv, po, pdo, plse, _ptr(bias, 4, "bias"),
-                                                _ptr(land, 4, "land"), pdq, pdk, pdv, _ptr(dbias, 4, "dbias"),
-                                                _ptr(workspace, 256, "workspace"), ws_bytes, drop, _handle(stream)),
-           "swin_attn_bwd_dropout")
+    _check(load_library().swin_attn_bwd_dropout(
+        plan.handle, *map(_addr, (q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, workspace)), ws_bytes, drop,
+        _handle(stream)), "swin_attn_bwd_dropout")
 
 
 def _addr(t):
