@@ -100,6 +100,52 @@ __device__ __forceinline__ void axpy_row(float *acc, float p, const float *b_sme
   }
 }
 
+// Dots of one row in registers with rows j ... j + 3 of a tile: four independent
+// chains of fused multiply-adds, each in dot_row's order, so that the value of a
+// pair is the same bit for bit. (The tile has 128 rows; a row that no slot feeds
+// gives a value that nobody uses.)
+template <int HD>
+__device__ __forceinline__ void dot_rows4(const float *a, const float *tile, int j, float (&out)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[k] = 0.f;
+#pragma unroll
+  for (int c = 0; c < HD / 4; ++c)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 x = reinterpret_cast<const float4 *>(tile + (j + k) * HD)[c];
+      out[k] = fmaf(a[4 * c], x.x, out[k]);
+      out[k] = fmaf(a[4 * c + 1], x.y, out[k]);
+      out[k] = fmaf(a[4 * c + 2], x.z, out[k]);
+      out[k] = fmaf(a[4 * c + 3], x.w, out[k]);
+    }
+}
+
+// The two dots of pair (row, j) in a walk over j = 0, 1, ...: a0 with t0's row and a1
+// with t1's. With dropout four rows are taken at once: half the pairs of a warp
+// need the second dot anyway, and one chain of fused multiply-adds waits for itself
+// (backward, fp32, 180 x 360, window 6 x 12, 4 heads of 32: 1299 -> 1162 us; 16 x
+// 32, window 4 x 8, heads of 16: 39.6 -> 35.5). Without dropout a pair that the
+// mask leaves out is skipped whole, which is faster there (975 us against 1076).
+template <int HD, bool kFour>
+struct PairDots {
+  const float *a0, *t0, *a1, *t1;
+  float d0[4], d1[4];
+  __device__ __forceinline__ PairDots(const float *a0_, const float *t0_, const float *a1_, const float *t1_)
+      : a0(a0_), t0(t0_), a1(a1_), t1(t1_) {}
+  __device__ __forceinline__ void step(int j) {
+    if (kFour && (j & 3) == 0) {
+      dot_rows4<HD>(a0, t0, j, d0);
+      dot_rows4<HD>(a1, t1, j, d1);
+    }
+  }
+  static __device__ __forceinline__ float pick(const float (&v)[4], int j) {
+    const float a = (j & 1) ? v[1] : v[0], b = (j & 1) ? v[3] : v[2];
+    return (j & 2) ? b : a;
+  }
+  __device__ __forceinline__ float first(int j) const { return kFour ? pick(d0, j) : dot_row<HD>(a0, t0 + j * HD); }
+  __device__ __forceinline__ float second(int j) const { return kFour ? pick(d1, j) : dot_row<HD>(a1, t1 + j * HD); }
+};
+
 __host__ __device__ inline int round4(int x) { return (x + 3) & ~3; }
 
 // ---- forward --------------------------------------------------------------
@@ -306,17 +352,20 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
           sKeep[tid * 5 + w] = bits;
         }
       }
+      PairDots<HD, kDrop> dots(qi, sK, doi, sV);
       for (int j = 0; j < g.n; ++j) {
+        dots.step(j);
         if (sKcode[j] != r.reg) continue;
-        const float s = dot_row<HD>(qi, sK + j * HD) * a.scale + sB[r.rbase - sRoff[j]];
+        const float s = dots.first(j) * a.scale + sB[r.rbase - sRoff[j]];
         // the kept values' scale is left out of dP and dS here; dq, dk, dv and dBias take it at the end
-        if (kept(tid, j)) delta = fmaf(expf(s - lse), dot_row<HD>(doi, sV + j * HD), delta);
+        if (kept(tid, j)) delta = fmaf(expf(s - lse), dots.second(j), delta);
       }
       for (int j = 0; j < g.n; ++j) {
+        dots.step(j);
         if (sKcode[j] != r.reg) continue;
-        const float s = dot_row<HD>(qi, sK + j * HD) * a.scale + sB[r.rbase - sRoff[j]];
+        const float s = dots.first(j) * a.scale + sB[r.rbase - sRoff[j]];
         const float p = expf(s - lse);
-        const float ds = p * ((kept(tid, j) ? dot_row<HD>(doi, sV + j * HD) : 0.f) - delta);
+        const float ds = p * ((kept(tid, j) ? dots.second(j) : 0.f) - delta);
         axpy_row<HD>(dq, ds, sK + j * HD);
         sPart[tid * kPartStride + j] += ds;
       }
@@ -341,12 +390,14 @@ __global__ void __launch_bounds__(kThreads) bwd_simt_kernel(const BwdArgs a) {
           kj[c] = sK[tid * HD + c];
           vj[c] = sV[tid * HD + c];
         }
+        PairDots<HD, kDrop> dots(kj, sQ, vj, sdO);
         for (int i = 0; i < g.n; ++i) {
+          dots.step(i);
           if (sQcode[i] != r.reg) continue;
-          const float s = dot_row<HD>(kj, sQ + i * HD) * a.scale + sB[sRbase[i] - r.roff];
+          const float s = dots.first(i) * a.scale + sB[sRbase[i] - r.roff];
           const float p = expf(s - sLse[i]);
           const bool keep = kept(i, tid);
-          const float ds = p * ((keep ? dot_row<HD>(vj, sdO + i * HD) : 0.f) - sDelta[i]);
+          const float ds = p * ((keep ? dots.second(i) : 0.f) - sDelta[i]);
           axpy_row<HD>(dk, ds, sQ + i * HD);
           if (keep) axpy_row<HD>(dv, p, sdO + i * HD);
         }
