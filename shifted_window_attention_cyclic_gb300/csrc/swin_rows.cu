@@ -161,23 +161,23 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
   Philox ph;
   ph.init(d);
   const int64_t nvec = (n + 7) >> 3;
-  const bool narrow = n <= INT32_MAX && span <= INT32_MAX;  // 32-bit division: a quarter of the long one's work
+  const bool narrow = n <= UINT32_MAX;  // 32-bit division: a quarter of the long one's work
   for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < nvec; v += (int64_t)gridDim.x * 256) {
     const int64_t i0 = v * 8;
-    uint32_t keep = 0xFFu;  // bit e: element i0 + e keeps
+    uint4 own = make_uint4(0u, 0u, 0u, 0u);  // modes 0 and 1: numbers compared where they are used (as bits: 201 us)
+    uint32_t keep = 0u;                      // mode 2, bit e: element i0 + e keeps
     if (kMode == 0) {
-      keep = keep_bits(ph.block((uint64_t)v), d.thr);
+      own = ph.block((uint64_t)v);
     } else {
-      const int64_t first = narrow ? (uint32_t)i0 / (uint32_t)span : i0 / span;
+      const int64_t first = narrow ? (uint32_t)i0 / (uint32_t)min(span, (int64_t)UINT32_MAX) : i0 / span;
       if (kMode == 1) {
-        if (!keep_one(ph, (uint64_t)first, d.thr)) keep = 0u;
+        if (keep_one(ph, (uint64_t)first, d.thr)) own = make_uint4(~0u, ~0u, ~0u, ~0u);
       } else {
         const uint64_t at[2] = {(uint64_t)first >> 3, ((uint64_t)first >> 3) + 1};
         uint4 r[2];
         ph.blocks(at, r);
         uint32_t bits = (keep_bits(r[0], d.thr) | keep_bits(r[1], d.thr) << 8) >> (first & 7);
         int64_t left = span - (i0 - first * span);  // elements of the decision still to come
-        keep = 0u;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           keep |= (bits & 1u) << e;
@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         f[e] = mul(f[e], both(d.scale));
-        f[e] = make_float2((keep >> (2 * e)) & 1u ? f[e].x : 0.f, (keep >> (2 * e + 1)) & 1u ? f[e].y : 0.f);
+        if (kMode < 2) f[e] = kept(own, e, d.thr, f[e]);
+        else f[e] = make_float2((keep >> (2 * e)) & 1u ? f[e].x : 0.f, (keep >> (2 * e + 1)) & 1u ? f[e].y : 0.f);
       }
       Raw<T> out;
       pack(f, out);
@@ -204,7 +205,10 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (i0 + e < n) y[i0 + e] = (T)((keep >> e) & 1u ? (float)x[i0 + e] * d.scale : 0.f);
+        if (i0 + e < n) {
+          const bool k = kMode < 2 ? keep_of(own, e, d.thr) : (keep >> e) & 1u;
+          y[i0 + e] = (T)(k ? (float)x[i0 + e] * d.scale : 0.f);
+        }
     }
   }
 }

@@ -139,7 +139,11 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int TPR, int NT, int NV, int kStages>
+// Threads of a row: TPR, or where a row is a CTA of as many warps as it needs, the CTA's.
+template <int TPR, bool kFull>
+__device__ __forceinline__ int threads_of_row() { return kFull ? TPR : (int)blockDim.x; }
+
+template <typename T, int TPR, bool kFull, int NT, int NV, int kStages>
 struct Ring {
   static constexpr int kThreads = TPR > 32 ? TPR : 256;  // a wide row's CTA may have fewer
   static constexpr int kPieces = vec_bytes<T>() / 16;
@@ -152,7 +156,7 @@ struct Ring {
   int tpr;           // threads of a row
 
   __device__ __forceinline__ void init(uint8_t *smem, int lane, int C8) {
-    tpr = TPR > 32 ? (int)blockDim.x : TPR;
+    tpr = threads_of_row<TPR, kFull>();
     const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const int t = threadIdx.x, w = t & ~31, l = t & 31;  // 16-byte chunks of fp32: 64 a warp, 2 l and 2 l + 1 a lane
     if constexpr (kPieces == 1) {
@@ -272,13 +276,13 @@ __device__ __forceinline__ void draw_row(const Philox &ph, uint64_t vec, int ste
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
 __device__ __forceinline__ float shuffle_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
 __device__ __forceinline__ float2 shuffle_xor(float2 v, int o) { return make_float2(shuffle_xor(v.x, o), shuffle_xor(v.y, o)); }
-template <int TPR, typename V>
+template <int TPR, bool kFull, typename V>
 __device__ __forceinline__ V row_sum(V v, float2 *xchg, int &turn) {
 #pragma unroll
   for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v = add(v, shuffle_xor(v, o));
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;  // at most
-    const int warps = blockDim.x >> 5;
+    const int warps = threads_of_row<TPR, kFull>() >> 5;
     V *buf = reinterpret_cast<V *>(xchg + turn * W);
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
@@ -350,12 +354,12 @@ __device__ __forceinline__ int trips(const Place &p, int count) {
 // rate): HBM. Join of 138 240 x 512 bf16 with both norms, gate, scale and dropout:
 // 109 us, 5.2 TB/s (77 %): 16 warps an SM (128 registers) issue in 56 % of the
 // cycles and wait on the two norms' sums in turn.
-template <typename T, int TPR, int NV, bool kBranch, bool kPre>
+template <typename T, int TPR, bool kFull, int NV, bool kBranch, bool kPre>
 __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false, kBranch)) rows_fwd_kernel(const RowArgs a) {
   using S = Shape<T, TPR, NV, false, kBranch, kPre>;
-  const int tpr = TPR > 32 ? (int)blockDim.x : TPR;
+  const int tpr = threads_of_row<TPR, kFull>();
   constexpr int D = S::ahead, VB = vec_bytes<T>();
-  using R = Ring<T, TPR, S::tensors, NV, D + 1>;
+  using R = Ring<T, TPR, kFull, S::tensors, NV, D + 1>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
   int turn = 0;
@@ -441,8 +445,8 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false, k
 #pragma unroll
         for (int j = 0; j < NV; ++j) ring.read(out, 1, j, u[j]);
         if (post) {
-          if (a.post.kind == SWIN_NORM_LAYER) centre<NV>(u, row_sum<TPR>(sum_of<NV>(u), xchg, turn) * inv, ok);
-          const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(u, u), xchg, turn), inv, a.post.eps)));
+          if (a.post.kind == SWIN_NORM_LAYER) centre<NV>(u, row_sum<TPR, kFull>(sum_of<NV>(u), xchg, turn) * inv, ok);
+          const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR, kFull>(dot_of<NV>(u, u), xchg, turn), inv, a.post.eps)));
 #pragma unroll
           for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -469,8 +473,8 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false, k
       }
       out = R::next(out);
       if constexpr (kPre) {
-        if (a.pre.kind == SWIN_NORM_LAYER) centre<NV>(v, row_sum<TPR>(sum_of<NV>(v), xchg, turn) * inv, ok);
-        const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(v, v), xchg, turn), inv, a.pre.eps)));
+        if (a.pre.kind == SWIN_NORM_LAYER) centre<NV>(v, row_sum<TPR, kFull>(sum_of<NV>(v), xchg, turn) * inv, ok);
+        const float2 rstd = both(rsqrtf(fmaf(row_sum<TPR, kFull>(dot_of<NV>(v, v), xchg, turn), inv, a.pre.eps)));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           Raw<T> o;
@@ -489,10 +493,10 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, false, k
 // ---- backward ----------------------------------------------------------------
 // Sums the CTA's copies of this thread's channels of two column sums, writes
 // them (one: dst[0, C), zero: dst[C, 2 C)) and clears them.
-template <int TPR, int NV>
+template <int TPR, bool kFull, int NV>
 __device__ __forceinline__ void flush(float2 (&one)[NV][4], float2 (&zero)[NV][4], float *dst, int C8, float *buf) {
   constexpr int kThreads = block_of(TPR);
-  const int tpr = TPR > 32 ? (int)blockDim.x : TPR;
+  const int tpr = threads_of_row<TPR, kFull>();
   const int lane = TPR > 32 ? (int)threadIdx.x : (int)threadIdx.x % TPR;
   auto put = [&](float *p, const float2 (&v)[4]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
@@ -534,12 +538,12 @@ __device__ __forceinline__ void flush(float2 (&one)[NV][4], float2 (&zero)[NV][4
 // 5.9 TB/s (87 %). Join of 2 x 64 800 x 256 bf16 (LayerNorms, gate, scale, dropout,
 // path): 84 us, 4.7 TB/s (70 %): 238 registers leave 8 warps an SM, which issue in
 // 47 % of the cycles and wait on four rounds of row sums and on the generator.
-template <typename T, int TPR, int NV, bool kBranch, bool kPre>
+template <typename T, int TPR, bool kFull, int NV, bool kBranch, bool kPre>
 __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kBranch)) rows_bwd_kernel(const RowArgs a) {
   using S = Shape<T, TPR, NV, true, kBranch, kPre>;
-  const int tpr = TPR > 32 ? (int)blockDim.x : TPR;
+  const int tpr = threads_of_row<TPR, kFull>();
   constexpr int D = S::ahead, VB = vec_bytes<T>();
-  using R = Ring<T, TPR, S::tensors, NV, D + 1>;
+  using R = Ring<T, TPR, kFull, S::tensors, NV, D + 1>;
   constexpr int tDy = 0, tY = 1, tDh = 2, tZ = kPre ? 3 : 1;  // tensors of a stage
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 xchg[TPR > 32 ? 2 * (TPR / 32) : 1];
@@ -644,24 +648,24 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
       if constexpr (kPre && kBranch) {
         if (post) {
           if (pre_layer || post_layer) {
-            const float2 m = row_sum<TPR>(make_float2(sum_of<NV>(y), sum_of<NV>(z)), xchg, turn);
+            const float2 m = row_sum<TPR, kFull>(make_float2(sum_of<NV>(y), sum_of<NV>(z)), xchg, turn);
             if (pre_layer) centre<NV>(y, m.x * inv, ok);
             if (post_layer) centre<NV>(z, m.y * inv, ok);
           }
-          const float2 q = row_sum<TPR>(make_float2(dot_of<NV>(y, y), dot_of<NV>(z, z)), xchg, turn);
+          const float2 q = row_sum<TPR, kFull>(make_float2(dot_of<NV>(y, y), dot_of<NV>(z, z)), xchg, turn);
           y_rstd = rsqrtf(fmaf(q.x, inv, a.pre.eps));
           z_rstd = rsqrtf(fmaf(q.y, inv, a.post.eps));
         }
       }
       if constexpr (kPre)
         if (!kBranch || !post) {
-          if (pre_layer) centre<NV>(y, row_sum<TPR>(sum_of<NV>(y), xchg, turn) * inv, ok);
-          y_rstd = rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(y, y), xchg, turn), inv, a.pre.eps));
+          if (pre_layer) centre<NV>(y, row_sum<TPR, kFull>(sum_of<NV>(y), xchg, turn) * inv, ok);
+          y_rstd = rsqrtf(fmaf(row_sum<TPR, kFull>(dot_of<NV>(y, y), xchg, turn), inv, a.pre.eps));
         }
       if constexpr (kBranch && !kPre)
         if (post) {
-          if (post_layer) centre<NV>(z, row_sum<TPR>(sum_of<NV>(z), xchg, turn) * inv, ok);
-          z_rstd = rsqrtf(fmaf(row_sum<TPR>(dot_of<NV>(z, z), xchg, turn), inv, a.post.eps));
+          if (post_layer) centre<NV>(z, row_sum<TPR, kFull>(sum_of<NV>(z), xchg, turn) * inv, ok);
+          z_rstd = rsqrtf(fmaf(row_sum<TPR, kFull>(dot_of<NV>(z, z), xchg, turn), inv, a.post.eps));
         }
       float2 g[NV][4];  // dy, then dy' = dx
 #pragma unroll
@@ -689,9 +693,9 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
         float2 c = make_float2(dot_of<NV>(dh, y), 0.f);
         if (pre_layer) {
           c.y = sum_of<NV>(dh);
-          c = row_sum<TPR>(c, xchg, turn);
+          c = row_sum<TPR, kFull>(c, xchg, turn);
         } else {
-          c.x = row_sum<TPR>(c.x, xchg, turn);
+          c.x = row_sum<TPR, kFull>(c.x, xchg, turn);
         }
         const float2 c1 = both(-c.x * inv);
 #pragma unroll
@@ -736,9 +740,9 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
             float2 c = make_float2(dot_of<NV>(g, z), 0.f);
             if (post_layer) {
               c.y = sum_of<NV>(g);
-              c = row_sum<TPR>(c, xchg, turn);
+              c = row_sum<TPR, kFull>(c, xchg, turn);
             } else {
-              c.x = row_sum<TPR>(c.x, xchg, turn);
+              c.x = row_sum<TPR, kFull>(c.x, xchg, turn);
             }
             const float2 c1 = both(-c.x * inv), c0 = both(-c.y * inv);
 #pragma unroll
@@ -767,7 +771,7 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
     if constexpr (kBranch)
       if (a.part_post && (a.gate || s == last)) {
         float *dst = a.part_post + ((int64_t)blockIdx.x + (a.gate ? b : 0)) * 2 * a.C;
-        flush<TPR, NV>(b1, b0, dst, C8, reinterpret_cast<float *>(smem));
+        flush<TPR, kFull, NV>(b1, b0, dst, C8, reinterpret_cast<float *>(smem));
         if (TPR <= 32) __syncthreads();  // the ring takes the buffer again
       }
   }
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(block_of(TPR), blocks_per_sm(TPR, NV, true, kB
   if constexpr (kPre)
     if (a.part_pre) {
       float *dst = a.part_pre + (int64_t)blockIdx.x * 2 * a.C;
-      flush<TPR, NV>(a1, a0, dst, C8, reinterpret_cast<float *>(smem));
+      flush<TPR, kFull, NV>(a1, a0, dst, C8, reinterpret_cast<float *>(smem));
     }
 }
 
@@ -844,12 +848,16 @@ template <typename T, int TPR, int NV, bool kBwd, bool kBranch, bool kPre>
 int launch_one(const RowArgs &a, int ctas, cudaStream_t st) {
   using S = Shape<T, TPR, NV, kBwd, kBranch, kPre>;
   void (*kern)(const RowArgs);
-  if constexpr (kBwd) kern = rows_bwd_kernel<T, TPR, NV, kBranch, kPre>;
-  else kern = rows_fwd_kernel<T, TPR, NV, kBranch, kPre>;
+  const int threads = threads_of(width_of(a.C, kBwd && kBranch && kPre), a.C);
+  // the backward of a CTA's rows is built for all the threads too: with their number from the launch it takes 2 % longer
+  // at 1024 channels, 4 % at 2048 and 7 % at 4096 (the forward: no longer)
+  if constexpr (!kBwd) kern = rows_fwd_kernel<T, TPR, TPR <= 32, NV, kBranch, kPre>;
+  else if constexpr (TPR <= 32) kern = rows_bwd_kernel<T, TPR, true, NV, kBranch, kPre>;
+  else kern = threads == TPR ? rows_bwd_kernel<T, TPR, true, NV, kBranch, kPre> : rows_bwd_kernel<T, TPR, false, NV, kBranch, kPre>;
   if (S::smem > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess)
     return SWIN_ERR_CUDA;
-  kern<<<ctas, threads_of(width_of(a.C, kBwd && kBranch && kPre), a.C), S::smem, st>>>(a);
+  kern<<<ctas, threads, S::smem, st>>>(a);
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }
 
