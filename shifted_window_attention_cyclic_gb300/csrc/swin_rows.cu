@@ -80,7 +80,10 @@ __device__ __forceinline__ Sums slot_sum(const float *part, int s0, int s1, int 
 // gradients and their gate-weighted sum. The pair (CTA r, image b) has slot
 // r + b, so image b owns the slots from its first row's CTA to its last row's.
 // A few images share the lanes; many take a lane each. Latency bound: 7 us with
-// cold caches, 3 to 6 us behind the row kernel, whose sums lie in L2.
+// cold caches, 3 to 6 us behind the row kernel, whose sums lie in L2. (Blocks of 8
+// channels and 128 lanes: join backward of 256 channels 1 to 2 us shorter, of
+// 4096 channels 8 longer; of 16 channels: 0 and 4. Eight slots loaded at once
+// under predicates: 2 us longer with 1024 channels, else the same.)
 __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a) {
   static_assert(kColLanes == 32, "a warp sums the lanes of a channel");
   // launched while the row kernel's last CTAs still run: their sums are there after this

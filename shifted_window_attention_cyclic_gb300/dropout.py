@@ -104,12 +104,13 @@ def apply_dropout(x, drop, span=1, out=None, stream=None):
         check_dropout("drop", drop, x.device)
     if out is not None:
         same_rows("out", out, x)
+    span = min(int(span), 2 ** 62)  # from x's size on they are all the same
     ctx = on(x.device, stream)
     if ctx is not None:
         with ctx:
             return apply_dropout(x, drop, span, out)
     out = torch.empty_like(x) if out is None else out
-    C.swin_attn_dropout(_C_DTYPE[x.dtype], x.numel(), int(span), x, drop.desc if drop else None, out)
+    C.swin_attn_dropout(_C_DTYPE[x.dtype], x.numel(), span, x, drop.desc if drop else None, out)
     return out
 
 
