@@ -221,9 +221,15 @@ constexpr int block_of(int tpr) { return tpr > 32 ? tpr : 256; }
 // sums, two parameters and four rows of 8 channels are 80 registers a vector
 // before any address, so 512 threads of one vector with 128 registers, or 256
 // of two or three. (640 threads with 96 registers spilled: 1-degree join backward
-// 101 us against 91; 768 threads for the norm alone gained nothing.)
+// 101 us against 91; 768 threads for the norm alone gained nothing.) A row that
+// is a CTA's waits in every round of its sums, so two CTAs an SM pay more than
+// registers: the norm alone in 128 (75 M bf16 elements in 4096 channels 126 -> 107
+// us, in 3584 138 -> 109), and a CTA of 160 threads, 2049 to 2560 bf16 channels,
+// in 168 (10 warps are three on a scheduler), of which both norms' join spills
+// 24: 2056 channels, norm 221 -> 139 us, join without a norm after it 213 -> 117,
+// with both norms and dropout 433 -> 321.
 constexpr int blocks_per_sm(int tpr, int nv, bool bwd, bool branch) {
-  const int threads = bwd ? (nv == 1 ? 512 : 256) : nv == 3 ? (branch ? 256 : 512) : nv == 2 ? 512 : branch ? 768 : 1024;
+  const int threads = bwd ? (tpr == 160 ? 320 : nv == 1 || (tpr == 256 && !branch) ? 512 : 256) : nv == 3 ? (branch ? 256 : 512) : nv == 2 ? 512 : branch ? 768 : 1024;
   return threads > block_of(tpr) ? threads / block_of(tpr) : 1;
 }
 
@@ -795,10 +801,13 @@ struct Width {
 // (three, of 75 M elements: 384 channels, join 103 us against 128 with two,
 // norm backward 103 against 115; 768 channels, join 108 us against 142 with a
 // CTA's three warps a row). Above, a row is a CTA's, with as many warps as it
-// needs, one vector a thread up to 2048 channels, two from there. Of the backward
+// needs, one vector a thread up to 2048 channels, two from there. (fp32 rows of 2049
+// to 2560 channels stay with the bound of 256 threads: twice the bytes a row keep
+// HBM busy, and the join backward with both norms took 246 us against 232 in 168
+// registers.) Of the backward
 // with both norms three vectors spill: they pay between 129 and 192 and between
 // 257 and 384 channels, where a third of the lanes would idle.
-inline Width width_of(int C, bool both_backward) {
+inline Width width_of(int C, bool both_backward, bool bf16) {
   const int c8 = C >> 3;
   if (c8 <= 2) return {2, 1};
   if (c8 <= 4) return {4, 1};
@@ -812,6 +821,7 @@ inline Width width_of(int C, bool both_backward) {
   if (c8 <= 96 && !both_backward) return {32, 3};
   if (c8 <= 128) return {128, 1};
   if (c8 <= 256) return {256, 1};
+  if (c8 <= 320 && bf16) return {160, 2};
   if (c8 <= 512) return {256, 2};
   return {512, 2};
 }
@@ -829,12 +839,15 @@ struct Split {
 // Consecutive rows per CTA, as many CTAs as fit on the GPU at once (a wide row's
 // CTA with fewer warps than its kernel is bounded for leaves room for more).
 inline Split split_rows(int64_t rows, int C, int sms, bool bwd, bool branch, bool pre, bool bf16) {
-  const Width wd = width_of(C, bwd && branch && pre);
+  const Width wd = width_of(C, bwd && branch && pre, bf16);
   const int threads = threads_of(wd, C), most = block_of(wd.tpr);
   int per_sm = blocks_per_sm(wd.tpr, wd.nv, bwd, branch);
   if (threads < most) {
     const int smem = smem_of(wd.tpr, wd.nv, bwd, branch, pre, bf16 ? 2 : 4);
-    per_sm = std::max(per_sm, std::min(per_sm * most / threads, 200 * 1024 / smem));
+    // threads an SM: what the kernel is bounded for; the norm's backward takes fewer registers than its bound (88 to 96:
+    // 1392 channels 156 -> 138 us)
+    const int fit = bwd && !branch && wd.nv == 1 ? 640 : per_sm * most;
+    per_sm = std::max(per_sm, std::min(fit / threads, 200 * 1024 / smem));
   }
   const int64_t at_once = wd.tpr > 32 ? 1 : threads / wd.tpr;
   const int64_t groups = (rows + at_once - 1) / at_once;
@@ -848,11 +861,12 @@ template <typename T, int TPR, int NV, bool kBwd, bool kBranch, bool kPre>
 int launch_one(const RowArgs &a, int ctas, cudaStream_t st) {
   using S = Shape<T, TPR, NV, kBwd, kBranch, kPre>;
   void (*kern)(const RowArgs);
-  const int threads = threads_of(width_of(a.C, kBwd && kBranch && kPre), a.C);
+  const int threads = threads_of(width_of(a.C, kBwd && kBranch && kPre, sizeof(T) == 2), a.C);
   // the backward of a CTA's rows is built for all the threads too: with their number from the launch it takes 2 % longer
   // at 1024 channels, 4 % at 2048 and 7 % at 4096 (the forward: no longer)
-  if constexpr (!kBwd) kern = rows_fwd_kernel<T, TPR, TPR <= 32, NV, kBranch, kPre>;
-  else if constexpr (TPR <= 32) kern = rows_bwd_kernel<T, TPR, true, NV, kBranch, kPre>;
+  constexpr bool kAll = TPR <= 32 || TPR == 160;
+  if constexpr (!kBwd) kern = rows_fwd_kernel<T, TPR, kAll, NV, kBranch, kPre>;
+  else if constexpr (kAll) kern = rows_bwd_kernel<T, TPR, true, NV, kBranch, kPre>;
   else kern = threads == TPR ? rows_bwd_kernel<T, TPR, true, NV, kBranch, kPre> : rows_bwd_kernel<T, TPR, false, NV, kBranch, kPre>;
   if (S::smem > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) != cudaSuccess)
@@ -875,7 +889,7 @@ int launch_rows(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cud
 
 template <typename T>
 int launch_width(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
-  const Width wd = width_of(a.C, bwd && branch && pre);
+  const Width wd = width_of(a.C, bwd && branch && pre, sizeof(T) == 2);
   if (wd.tpr == 2) return launch_rows<T, 2, 1>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 4 && wd.nv == 1) return launch_rows<T, 4, 1>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 4 && wd.nv == 2) return launch_rows<T, 4, 2>(a, bwd, branch, pre, ctas, st);
@@ -887,6 +901,8 @@ int launch_width(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cu
   if (wd.tpr == 32 && wd.nv == 2) return launch_rows<T, 32, 2>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 32) return launch_rows<T, 32, 3>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 128) return launch_rows<T, 128, 1>(a, bwd, branch, pre, ctas, st);
+  if constexpr (sizeof(T) == 2)
+    if (wd.tpr == 160) return launch_rows<T, 160, 2>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 256 && wd.nv == 1) return launch_rows<T, 256, 1>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 256) return launch_rows<T, 256, 2>(a, bwd, branch, pre, ctas, st);
   return launch_rows<T, 512, 2>(a, bwd, branch, pre, ctas, st);

@@ -117,7 +117,7 @@ PRESENT = [ALL, (), ("scale", "pre_gamma"), ("gate", "post_gamma"), ("post_beta"
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("post,pre", JOINS)
-@pytest.mark.parametrize("channels", [8, 56, 96, 168, 256, 376, 512, 648, 1024, 1600, 2056, 5128, 8192])
+@pytest.mark.parametrize("channels", [8, 56, 96, 168, 256, 376, 512, 648, 1024, 1600, 2056, 2560, 3848, 5128, 8192])
 def test_join(channels, post, pre, dtype):
     from shifted_window_attention_cyclic_gb300.residual import ResidualJoin
     join = ResidualJoin(channels, post, pre, 1e-5, dtype)
