@@ -10,9 +10,9 @@ backward is done.
 from __future__ import annotations
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import swin_attn as C
+from .autograd import once_differentiable
 
 _C_DTYPE = {torch.bfloat16: C.SWIN_BF16, torch.float32: C.SWIN_F32}
 
@@ -117,7 +117,7 @@ def apply_dropout(x, drop, span=1, out=None, stream=None):
 class _DropoutFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, drop, span):
-        ctx.drop, ctx.span = drop, span
+        ctx.drop, ctx.span, ctx.linear = drop, span, True
         if drop is not None:
             ctx.save_for_backward(drop.state.tensor)  # a state advanced before the backward is reported
         return apply_dropout(x.contiguous(), drop, span)

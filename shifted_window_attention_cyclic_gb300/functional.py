@@ -10,6 +10,7 @@ from contextlib import nullcontext
 import torch
 
 from . import swin_attn as C
+from .autograd import once_differentiable
 from .dropout import check_dropout
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -185,6 +186,7 @@ class _SwinAttnFn(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, bias, land, lse, o, _ = ctx.saved_tensors
         want_dbias = bias is not None and ctx.needs_input_grad[4]

@@ -15,9 +15,9 @@ import math
 from collections import namedtuple
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import swin_attn as C
+from .autograd import once_differentiable
 from .dropout import check_dropout, on, same_rows
 from .functional import _TORCH_DTYPE, check_tensor
 
@@ -232,6 +232,7 @@ class _JoinFn(torch.autograd.Function):
         params = (post_gamma, post_beta, scale, gate, pre_gamma, pre_beta)
         y, h = join.forward(x, z, *params, drop=drop, path=path)
         ctx.join, ctx.drop, ctx.path = join, drop, path
+        ctx.linear = join.post == join.pre == "none" and not any(ctx.needs_input_grad[3:9])
         ctx.set_materialize_grads(False)
         # the states are saved so that one advanced before the backward is reported
         ctx.save_for_backward(y, z, *params, *(d.state.tensor if d else None for d in (drop, path)))
