@@ -92,6 +92,8 @@ class SwinWindowAttention:
         return self.plan.info
 
     def workspace(self):
+        """A workspace kept by this module, for callers of the library's own entry points; calls that use it
+        must not overlap."""
         nbytes = C.swin_attn_workspace_bytes(self.plan)
         if self._ws is None or self._ws.numel() < nbytes:
             self._ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
@@ -137,13 +139,11 @@ class SwinWindowAttention:
         dv = torch.empty_like(v) if dv is None else dv
         if dbias is None and want_dbias:
             dbias = torch.empty(self.bias_shape, dtype=torch.float32, device=self.device)  # overwritten
-        if drop is not None:
-            # a workspace of the call's own, on its stream: calls and captured graphs may overlap
-            nbytes = max(C.swin_attn_workspace_bytes(self.plan), 256)
-            with torch.cuda.stream(stream) if stream is not None else nullcontext():
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        else:
-            ws = self.workspace()  # dBias partial tables; for head_dim 128 also delta
+        # dBias partial tables, for head_dim 128 also delta: the call's own, on its stream (calls and captured graphs
+        # of one module may overlap)
+        nbytes = max(C.swin_attn_workspace_bytes(self.plan), 256)
+        with torch.cuda.stream(stream) if stream is not None else nullcontext():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         if drop is not None:
             C.swin_attn_bwd_dropout(self.plan, q, k, v, o, dout, lse, bias, land if self.has_land else None, dq, dk, dv,
                                     dbias, ws, drop, stream)
