@@ -5,13 +5,11 @@ single calls into the CUDA library (swin_attn_fwd, swin_attn_bwd).
 """
 from __future__ import annotations
 
-from contextlib import nullcontext
-
 import torch
 
 from . import swin_attn as C
 from .autograd import once_differentiable
-from .dropout import check_dropout
+from .dropout import check_dropout, on
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 
@@ -113,15 +111,19 @@ class SwinWindowAttention:
         """(O, log-sum-exp). `dropout` (a Dropout) drops softmax probabilities."""
         drop = self._check_dropout(dropout)
         self._check(q=q, k=k, v=v, bias=bias, land=land, o=o, lse=lse)
+        ctx = on(self.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.forward(q, k, v, bias, land, o, lse, need_lse, dropout=dropout)
         if o is None:
             o = torch.empty(self.shape, dtype=self.torch_dtype, device=self.device)
         if lse is None and need_lse:
             lse = torch.empty(self.lse_shape, dtype=torch.float32, device=self.device)
         land = land if self.has_land else None
         if drop is None:
-            C.swin_attn_fwd(self.plan, q, k, v, bias, land, o, lse, stream)
+            C.swin_attn_fwd(self.plan, q, k, v, bias, land, o, lse)
         else:
-            C.swin_attn_fwd_dropout(self.plan, q, k, v, bias, land, o, lse, drop, stream)
+            C.swin_attn_fwd_dropout(self.plan, q, k, v, bias, land, o, lse, drop)
         return o, lse
 
     def backward(self, q, k, v, dout, lse, bias=None, land=None, dq=None, dk=None, dv=None, dbias=None,
@@ -134,27 +136,26 @@ class SwinWindowAttention:
             raise ValueError("lse: the backward needs the forward's log-sum-exp")
         self._check(q=q, k=k, v=v, dout=dout, lse=lse, bias=bias, land=land, dq=dq, dk=dk, dv=dv, dbias=dbias,
                     o=o)
+        ctx = on(self.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.backward(q, k, v, dout, lse, bias, land, dq, dk, dv, dbias, want_dbias, o=o, dropout=dropout)
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
         dv = torch.empty_like(v) if dv is None else dv
         if dbias is None and want_dbias:
             dbias = torch.empty(self.bias_shape, dtype=torch.float32, device=self.device)  # overwritten
-        # dBias partial tables, for head_dim 128 also delta: the call's own, on its stream (calls and captured graphs
-        # of one module may overlap)
-        nbytes = max(C.swin_attn_workspace_bytes(self.plan), 256)
-        with torch.cuda.stream(stream) if stream is not None else nullcontext():
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        # dBias partial tables, for head_dim 128 also delta: the call's own (calls and captured graphs of one module
+        # may overlap)
+        ws = torch.empty(max(C.swin_attn_workspace_bytes(self.plan), 256), dtype=torch.uint8, device=self.device)
+        land = land if self.has_land else None
         if drop is not None:
-            C.swin_attn_bwd_dropout(self.plan, q, k, v, o, dout, lse, bias, land if self.has_land else None, dq, dk, dv,
-                                    dbias, ws, drop, stream)
+            C.swin_attn_bwd_dropout(self.plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, ws, drop)
         elif o is None:
-            C.swin_attn_bwd(self.plan, q, k, v, dout, lse, bias, land if self.has_land else None, dq, dk, dv, dbias,
-                            ws, stream)
+            C.swin_attn_bwd(self.plan, q, k, v, dout, lse, bias, land, dq, dk, dv, dbias, ws)
         else:
-            C.swin_attn_bwd_o(self.plan, q, k, v, o, dout, lse, bias, land if self.has_land else None, dq, dk, dv,
-                              dbias, ws, stream)
+            C.swin_attn_bwd_o(self.plan, q, k, v, o, dout, lse, bias, land, dq, dk, dv, dbias, ws)
         return dq, dk, dv, dbias
-
 
     def block_forward(self, x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, bias=None, land=None, ln_eps=1e-5,
                       y=None, stream=None):
@@ -168,10 +169,14 @@ class SwinWindowAttention:
                                    ("w_o", w_o, (c, c), torch.bfloat16), ("b_o", b_o, (c,), torch.float32)):
             if tuple(t.shape) != shape or t.dtype != dt or t.device != self.device or not t.is_contiguous():
                 raise ValueError("%s: want a contiguous %s %s on %s" % (name, dt, shape, self.device))
+        ctx = on(self.device, stream)
+        if ctx is not None:
+            with ctx:
+                return self.block_forward(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, bias, land, ln_eps, y)
         if y is None:
             y = torch.empty(self.shape, dtype=self.torch_dtype, device=self.device)
         C.swin_attn_block_fwd(self.plan, x, ln_gamma, ln_beta, ln_eps, w_qkv, b_qkv, w_o, b_o, bias,
-                              land if self.has_land else None, y, stream)
+                              land if self.has_land else None, y)
         return y
 
 

@@ -64,3 +64,30 @@ def test_two_streams_and_two_graphs(head_dim, grid, window, dtype, rate):
         torch.cuda.synchronize()
         for k, (_, out) in enumerate(graphs):
             same(out, want[k], head_dim)
+
+
+def stream_of(t):
+    """The stream that the memory of `t` was allocated on."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("rate", [None, 0.2])
+def test_outputs_belong_to_the_stream_they_are_written_on(rate):
+    from shifted_window_attention_cyclic_gb300.dropout import Dropout, DropoutState
+    from shifted_window_attention_cyclic_gb300.functional import SwinWindowAttention
+    attn = SwinWindowAttention((16, 32), (4, 8), (2, 4), (0, 1), 2, 32)
+    q, k, v, dout = (torch.randn(attn.shape, device="cuda").bfloat16() for _ in range(4))
+    bias = attn.new_bias()
+    drop = Dropout(DropoutState(9), rate, 4) if rate is not None else None
+    o, lse = attn.forward(q, k, v, bias, dropout=drop)
+    want = (o, lse) + attn.backward(q, k, v, dout, lse, bias, dropout=drop)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = attn.forward(q, k, v, bias, dropout=drop, stream=side)
+    got = (o2, lse2) + attn.backward(q, k, v, dout, lse2, bias, dropout=drop, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert {stream_of(t) for t in got} == {side.cuda_stream}
+    assert side.cuda_stream not in {stream_of(t) for t in want}
