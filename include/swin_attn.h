@@ -296,7 +296,9 @@ typedef struct {
 } swin_attn_rows;
 
 /* Bytes of device workspace the backward calls on these rows need for any
- * parameter gradient (0 for a bad descriptor). */
+ * parameter gradient (0 for a bad descriptor). They grow with the images for
+ * a gate alone: the norm and a join without a gate take the workspace of the
+ * same rows as one image ({1, images * tokens}). */
 size_t swin_attn_rows_workspace_bytes(const swin_attn_rows *rows);
 
 /* The norm before a block: h = N(x). norm->kind is not NONE.

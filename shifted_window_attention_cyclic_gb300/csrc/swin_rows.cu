@@ -260,9 +260,30 @@ bool overlap(const void *p, const void *q, size_t bytes) {
   return p && q && a < b + bytes && b < a + bytes;
 }
 
-// Column sums in the workspace: of the pre norm [ctas], of the join [ctas + images], of image groups.
-int64_t join_slots(int ctas, int64_t images) { return (int64_t)ctas + std::max<int64_t>(images, 1); }
+// Column sums in the workspace: of the pre norm [ctas], of the join [ctas + images with rows], of image groups.
+int64_t join_slots(int ctas, int64_t images, int64_t rows) {
+  return (int64_t)ctas + std::max<int64_t>(std::min(images, rows), 1);
+}
 int64_t image_groups(int64_t images) { return std::max<int64_t>(1, (images + kGroupImages - 1) / kGroupImages); }
+
+// Bytes of a backward's workspace, whichever of its kernels runs; images: 1 where there is no gate.
+size_t workspace_bytes_of(const swin_attn_rows *r, int64_t images, int sms) {
+  const int64_t rows = r->images * r->tokens;
+  int ctas = 0;
+  for (int k = 1; k < 4; ++k)
+    ctas = std::max(ctas, split_rows(rows, r->channels, sms, true, k & 1, k & 2, r->dtype == SWIN_BF16).ctas);
+  const size_t slots = (size_t)(ctas + join_slots(ctas, images, rows) + image_groups(images));
+  const size_t need = slots * 2 * r->channels * sizeof(float);
+  return (need + 255) & ~size_t(255);
+}
+
+// The images that a join's rows are cut by: where neither gate nor path looks at
+// them, one (every image a CTA meets costs it a drained and refilled ring).
+void cut_images(const swin_attn_rows *r, RowArgs *a) {
+  const bool any = a->gate || a->path.thr;
+  a->tokens = any ? r->tokens : a->rows;
+  a->images = any ? (int)r->images : 1;
+}
 
 }  // namespace
 }  // namespace swin
@@ -276,12 +297,7 @@ size_t swin_attn_rows_workspace_bytes(const swin_attn_rows *r) {
   size_t bytes = 0;
   int sms = 0;
   if (check_rows(r, &rows, &bytes) || sm_count(&sms)) return 0;
-  int ctas = 0;  // of whichever backward kernel
-  for (int k = 1; k < 4; ++k)
-    ctas = std::max(ctas, split_rows(rows, r->channels, sms, true, k & 1, k & 2, r->dtype == SWIN_BF16).ctas);
-  const size_t slots = (size_t)(ctas + join_slots(ctas, r->images) + image_groups(r->images));
-  const size_t need = slots * 2 * r->channels * sizeof(float);
-  return (need + 255) & ~size_t(255);
+  return workspace_bytes_of(r, r->images, sms);
 }
 
 int swin_attn_norm_fwd(const swin_attn_rows *r, const void *x, const swin_attn_norm *norm, void *h,
@@ -341,8 +357,7 @@ int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, co
   a.wide = !mis(y, 32) && !mis(h, 32);
   a.scale = join->scale;
   a.gate = join->gate;
-  a.tokens = r->tokens;
-  a.images = (int)r->images;
+  cut_images(r, &a);
   a.C = r->channels;
   const Split sp = split_rows(a.rows, a.C, sms, false, true, pre, r->dtype == SWIN_BF16);
   a.chunk = sp.chunk;
@@ -380,14 +395,13 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
   int rc = sm_count(&sms);
   if (rc) return rc;
   a.C = r->channels;
-  a.images = (int)r->images;
-  a.tokens = branch ? r->tokens : a.rows;  // the norm alone does not look at images
+  cut_images(r, &a);
   const int64_t groups = a.gate && want_post ? image_groups(a.images) : 1;
   if (groups > 65535) return SWIN_ERR_UNSUPPORTED;  // (a grid's y)
   const Split sp = split_rows(a.rows, a.C, sms, true, branch, pre, r->dtype == SWIN_BF16);
   a.chunk = sp.chunk;
   if (want_pre || want_post) {
-    if (!workspace || workspace_bytes < swin_attn_rows_workspace_bytes(r)) return SWIN_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < workspace_bytes_of(r, a.gate ? a.images : 1, sms)) return SWIN_ERR_WORKSPACE;
     if (mis(workspace, 256)) return SWIN_ERR_ALIGNMENT;
     float *ws = static_cast<float *>(workspace);
     a.part_pre = want_pre ? ws : nullptr;
@@ -424,7 +438,7 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
     c.dgate = g.gate;
   }
   const int tiles = (a.C + 31) / 32;
-  if (groups > 1) c.groups = a.part_post + join_slots(sp.ctas, a.images) * 2 * a.C;
+  if (groups > 1) c.groups = a.part_post + join_slots(sp.ctas, a.images, a.rows) * 2 * a.C;
   if ((rc = launch_columns(c, tiles, (unsigned)groups, st))) return rc;
   if (groups > 1) {  // the groups' sums are what a join without a gate would have left
     c.part_post = c.groups;

@@ -75,7 +75,10 @@ class _Rows:
                 same_rows(name, t, x)
 
     @staticmethod
-    def _workspace(rows, device):
+    def _workspace(rows, device, gated=False):
+        """For parameter gradients; without a gate, that of the rows as one image."""
+        if not gated:
+            rows = C.swin_attn_rows(1, rows.images * rows.tokens, rows.channels, rows.dtype)
         return torch.empty(max(C.swin_attn_rows_workspace_bytes(rows), 256), dtype=torch.uint8, device=device)
 
 
@@ -198,7 +201,7 @@ class ResidualJoin(_Rows):
                 return self.backward(y, z, dy, dh, *params, drop, path, want_params)
         dx, dz = torch.empty_like(y), torch.empty_like(y)
         grads = [torch.empty_like(p) if want_params and p is not None else None for p in params]
-        ws = self._workspace(rows, y.device) if any(g is not None for g in grads) else None
+        ws = self._workspace(rows, y.device, gate is not None) if any(g is not None for g in grads) else None
         C.swin_attn_join_bwd(rows, y, z, join, dy, dh, dx, dz, C.swin_attn_join_grads(*map(_addr, grads)), ws)
         return JoinGrads(dx, dz, *grads)
 
