@@ -273,9 +273,10 @@ int swin_attn_block_fwd(swin_attn_plan_t plan, const void *x, const float *ln_ga
  * flattened); no plan is needed. They run on the current device, to which
  * every pointer must belong, allocate nothing and are asynchronous on
  * `stream`. Activations are 16-byte, float parameters 4-byte, workspaces
- * 256-byte aligned (ALIGNMENT). An output may be exactly one of the call's
- * inputs of its own size (in place); outputs that overlap each other, or
- * partly an input, are INVALID_ARG. With no rows nothing is read or written
+ * 256-byte aligned (ALIGNMENT). An activation may be written exactly over an
+ * activation of the call, a parameter's gradient exactly over that parameter;
+ * any other overlap of an output or the workspace with another output or an
+ * input (a dropout's state too) is INVALID_ARG. With no rows nothing is read or written
  * but the parameter gradients, which are zero. All sums are fp32 in a fixed
  * order: the same inputs give the same bits. */
 

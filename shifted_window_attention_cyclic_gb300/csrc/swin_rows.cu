@@ -147,9 +147,11 @@ __global__ void __launch_bounds__(32 * kColLanes) columns_kernel(const ColArgs a
     a.groups[(int64_t)blockIdx.y * 2 * a.C + c] = all.one;
     a.groups[(int64_t)blockIdx.y * 2 * a.C + a.C + c] = all.zero;
   } else {
-    if (a.dpost_gamma) a.dpost_gamma[c] = a.kept * at(a.scale, c, 1.f) * all.one;
-    if (a.dpost_beta) a.dpost_beta[c] = a.kept * at(a.scale, c, 1.f) * all.zero;
-    if (a.dscale) a.dscale[c] = a.kept * fmaf(at(gamma, c, 1.f), all.one, at(beta, c, 0.f) * all.zero);
+    // every parameter is read before a gradient is written: each may lie on its parameter
+    const float scale = at(a.scale, c, 1.f), g = at(gamma, c, 1.f), b = at(beta, c, 0.f);
+    if (a.dpost_gamma) a.dpost_gamma[c] = a.kept * scale * all.one;
+    if (a.dpost_beta) a.dpost_beta[c] = a.kept * scale * all.zero;
+    if (a.dscale) a.dscale[c] = a.kept * fmaf(g, all.one, b * all.zero);
   }
 }
 
@@ -250,15 +252,32 @@ int check_norm(const swin_attn_norm &n, Norm *out) {
   return SWIN_OK;
 }
 
-// in may be exactly out; a partial overlap is refused
-bool clash(const void *in, const void *out, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(in), b = reinterpret_cast<uintptr_t>(out);
-  return in && out && a != b && a < b + bytes && b < a + bytes;
+// What a call reads or writes. An output may lie exactly on an input of its own
+// kind and size: an activation on an activation (each is read before its place
+// is written, by the same thread or warp), a parameter's gradient on that
+// parameter (the fold writes when nothing reads it any more). Any other overlap
+// would be a race.
+enum Kind { kActivation, kPostGamma, kPostBeta, kScale, kGate, kPreGamma, kPreBeta, kState, kWorkspace };
+struct Range {
+  const void *at;
+  size_t bytes;
+  Kind kind;
+};
+bool meet(const Range &a, const Range &b) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
+  return p && q && p < q + b.bytes && q < p + a.bytes;
 }
-bool overlap(const void *p, const void *q, size_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + bytes && b < a + bytes;
+template <int kOut, int kIn>
+bool clash(const Range (&out)[kOut], const Range (&in)[kIn]) {
+  for (int i = 0; i < kOut; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (const Range &r : in)
+      if (meet(out[i], r) && !(r.kind == out[i].kind && r.at == out[i].at && r.bytes == out[i].bytes)) return true;
+  }
+  return false;
 }
+Range state_of(const Drop &d) { return {d.state, 2 * sizeof(uint64_t), kState}; }
 
 // Column sums in the workspace: of the pre norm [ctas], of the join [ctas + images with rows], of image groups.
 int64_t join_slots(int ctas, int64_t images, int64_t rows) {
@@ -310,7 +329,11 @@ int swin_attn_norm_fwd(const swin_attn_rows *r, const void *x, const swin_attn_n
   rc = check_norm(*norm, &a.pre);
   if (rc) return rc;
   if (a.rows == 0) return SWIN_OK;
-  if (!x || !h || clash(x, h, bytes)) return SWIN_ERR_INVALID_ARG;
+  if (!x || !h) return SWIN_ERR_INVALID_ARG;
+  const size_t cb = sizeof(float) * r->channels;
+  const Range out[] = {{h, bytes, kActivation}};
+  const Range in[] = {{x, bytes, kActivation}, {norm->gamma, cb, kPreGamma}, {norm->beta, cb, kPreBeta}};
+  if (clash(out, in)) return SWIN_ERR_INVALID_ARG;
   if (mis(x, 16) || mis(h, 16)) return SWIN_ERR_ALIGNMENT;
   int sms = 0;
   rc = sm_count(&sms);
@@ -344,8 +367,19 @@ int swin_attn_join_fwd(const swin_attn_rows *r, const void *x, const void *z, co
   if (mis(join->scale, 4) || mis(join->gate, 4)) return SWIN_ERR_ALIGNMENT;
   if (a.rows == 0) return SWIN_OK;
   if (!x || !z || !y || (pre && !h)) return SWIN_ERR_INVALID_ARG;
-  if (clash(x, y, bytes) || clash(z, y, bytes) || clash(x, h, bytes) || clash(z, h, bytes) || overlap(y, h, bytes))
-    return SWIN_ERR_INVALID_ARG;
+  const size_t cb = sizeof(float) * r->channels;
+  const Range out[] = {{y, bytes, kActivation}, {h, bytes, kActivation}};
+  const Range in[] = {{x, bytes, kActivation},
+                      {z, bytes, kActivation},
+                      {join->post.gamma, cb, kPostGamma},
+                      {join->post.beta, cb, kPostBeta},
+                      {join->scale, cb, kScale},
+                      {join->gate, cb * r->images, kGate},
+                      {join->pre.gamma, cb, kPreGamma},
+                      {join->pre.beta, cb, kPreBeta},
+                      state_of(a.drop),
+                      state_of(a.path)};
+  if (clash(out, in)) return SWIN_ERR_INVALID_ARG;
   if (mis(x, 16) || mis(z, 16) || mis(y, 16) || mis(h, 16)) return SWIN_ERR_ALIGNMENT;
   int sms = 0;
   rc = sm_count(&sms);
@@ -465,9 +499,19 @@ int swin_attn_norm_bwd(const swin_attn_rows *r, const void *x, const swin_attn_n
   rc = check_norm(*norm, &a.pre);
   if (rc) return rc;
   if (mis(dgamma, 4) || mis(dbeta, 4)) return SWIN_ERR_ALIGNMENT;
+  if (a.rows && (!x || !dh || !dx)) return SWIN_ERR_INVALID_ARG;
+  const size_t cb = sizeof(float) * r->channels;
+  const Range out[] = {{dx, bytes, kActivation},
+                       {dgamma, cb, kPreGamma},
+                       {dbeta, cb, kPreBeta},
+                       {dgamma || dbeta ? workspace : nullptr, workspace_bytes, kWorkspace}};
+  const Range in[] = {{x, bytes, kActivation},
+                      {dh, bytes, kActivation},
+                      {dres, bytes, kActivation},
+                      {norm->gamma, cb, kPreGamma},
+                      {norm->beta, cb, kPreBeta}};
+  if (clash(out, in)) return SWIN_ERR_INVALID_ARG;
   if (a.rows) {
-    if (!x || !dh || !dx) return SWIN_ERR_INVALID_ARG;
-    if (clash(x, dx, bytes) || clash(dh, dx, bytes) || clash(dres, dx, bytes)) return SWIN_ERR_INVALID_ARG;
     if (mis(x, 16) || mis(dh, 16) || mis(dres, 16) || mis(dx, 16)) return SWIN_ERR_ALIGNMENT;
   }
   a.x = x;
@@ -504,13 +548,36 @@ int swin_attn_join_bwd(const swin_attn_rows *r, const void *y, const void *z, co
   const bool need_z = post || grads->scale || grads->gate;
   if (a.rows) {
     if ((!dy && !dh) || !dx || !dz || (need_z && !z) || (dh && !y)) return SWIN_ERR_INVALID_ARG;
-    const void *in[4] = {y, z, dy, dh};
-    for (const void *p : in) {
-      if (clash(p, dx, bytes) || clash(p, dz, bytes)) return SWIN_ERR_INVALID_ARG;
+  }
+  const size_t cb = sizeof(float) * r->channels, gb = cb * r->images;
+  const bool want = grads->post_gamma || grads->post_beta || grads->scale || grads->gate || grads->pre_gamma ||
+                    grads->pre_beta;
+  const Range out[] = {{dx, bytes, kActivation},
+                       {dz, bytes, kActivation},
+                       {grads->post_gamma, cb, kPostGamma},
+                       {grads->post_beta, cb, kPostBeta},
+                       {grads->scale, cb, kScale},
+                       {grads->gate, gb, kGate},
+                       {grads->pre_gamma, cb, kPreGamma},
+                       {grads->pre_beta, cb, kPreBeta},
+                       {want ? workspace : nullptr, workspace_bytes, kWorkspace}};
+  const Range in[] = {{y, bytes, kActivation},
+                      {z, bytes, kActivation},
+                      {dy, bytes, kActivation},
+                      {dh, bytes, kActivation},
+                      {join->post.gamma, cb, kPostGamma},
+                      {join->post.beta, cb, kPostBeta},
+                      {join->scale, cb, kScale},
+                      {join->gate, gb, kGate},
+                      {join->pre.gamma, cb, kPreGamma},
+                      {join->pre.beta, cb, kPreBeta},
+                      state_of(a.drop),
+                      state_of(a.path)};
+  if (clash(out, in)) return SWIN_ERR_INVALID_ARG;
+  if (a.rows) {
+    const void *act[6] = {y, z, dy, dh, dx, dz};
+    for (const void *p : act)
       if (mis(p, 16)) return SWIN_ERR_ALIGNMENT;
-    }
-    if (overlap(dx, dz, bytes)) return SWIN_ERR_INVALID_ARG;
-    if (mis(dx, 16) || mis(dz, 16)) return SWIN_ERR_ALIGNMENT;
   }
   if (!dh) a.pre.kind = SWIN_NORM_NONE;  // nothing reached h: its norm's gradients are zero
   a.x = y;
@@ -524,7 +591,6 @@ int swin_attn_join_bwd(const swin_attn_rows *r, const void *y, const void *z, co
   a.gate = join->gate;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (pre && !dh) {
-    const size_t cb = sizeof(float) * r->channels;
     if (grads->pre_gamma && cudaMemsetAsync(grads->pre_gamma, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
     if (grads->pre_beta && cudaMemsetAsync(grads->pre_beta, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
   }
@@ -540,7 +606,9 @@ int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, con
   if (rc) return rc;
   if (n == 0) return SWIN_OK;
   const size_t bytes = (size_t)n * (dtype == SWIN_BF16 ? 2 : 4);
-  if (!x || !y || clash(x, y, bytes)) return SWIN_ERR_INVALID_ARG;
+  if (!x || !y) return SWIN_ERR_INVALID_ARG;
+  const Range out[] = {{y, bytes, kActivation}}, in[] = {{x, bytes, kActivation}, state_of(d)};
+  if (clash(out, in)) return SWIN_ERR_INVALID_ARG;
   if (mis(x, 16) || mis(y, 16)) return SWIN_ERR_ALIGNMENT;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!d.thr) {  // rate 0
