@@ -37,3 +37,10 @@ def once_differentiable(backward):
         return _Refused.apply(torch.empty(0, requires_grad=True), *grads)
 
     return wrapper
+
+
+def usable(t):
+    """`t` as the library takes it, contiguous from a 16-byte boundary, or a copy that is (slices of larger tensors,
+    and the gradients that a concatenation hands back, start anywhere)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t

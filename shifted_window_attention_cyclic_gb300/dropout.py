@@ -12,7 +12,7 @@ from __future__ import annotations
 import torch
 
 from . import swin_attn as C
-from .autograd import once_differentiable
+from .autograd import once_differentiable, usable
 
 _C_DTYPE = {torch.bfloat16: C.SWIN_BF16, torch.float32: C.SWIN_F32}
 
@@ -120,13 +120,13 @@ class _DropoutFn(torch.autograd.Function):
         ctx.drop, ctx.span, ctx.linear = drop, span, True
         if drop is not None:
             ctx.save_for_backward(drop.state.tensor)  # a state advanced before the backward is reported
-        return apply_dropout(x.contiguous(), drop, span)
+        return apply_dropout(usable(x), drop, span)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         ctx.saved_tensors
-        return apply_dropout(dy.contiguous(), ctx.drop, ctx.span), None, None
+        return apply_dropout(usable(dy), ctx.drop, ctx.span), None, None
 
 
 def dropout(x, drop, span=1):

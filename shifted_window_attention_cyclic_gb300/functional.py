@@ -8,7 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import swin_attn as C
-from .autograd import once_differentiable
+from .autograd import once_differentiable, usable
 from .dropout import check_dropout, on
 
 _TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -183,7 +183,7 @@ class SwinWindowAttention:
 class _SwinAttnFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, attn, q, k, v, bias, land, dropout):
-        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        q, k, v = usable(q), usable(k), usable(v)
         o, lse = attn.forward(q, k, v, bias, land, dropout=dropout)
         ctx.attn, ctx.dropout = attn, dropout
         # the dropout's state is saved so that one advanced before the backward is reported
@@ -195,7 +195,7 @@ class _SwinAttnFn(torch.autograd.Function):
     def backward(ctx, dout):
         q, k, v, bias, land, lse, o, _ = ctx.saved_tensors
         want_dbias = bias is not None and ctx.needs_input_grad[4]
-        dq, dk, dv, dbias = ctx.attn.backward(q, k, v, dout.contiguous(), lse, bias, land, want_dbias=want_dbias,
+        dq, dk, dv, dbias = ctx.attn.backward(q, k, v, usable(dout), lse, bias, land, want_dbias=want_dbias,
                                               o=o, dropout=ctx.dropout)
         return None, dq, dk, dv, dbias, None, None
 

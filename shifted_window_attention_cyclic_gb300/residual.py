@@ -17,7 +17,7 @@ from collections import namedtuple
 import torch
 
 from . import swin_attn as C
-from .autograd import once_differentiable
+from .autograd import once_differentiable, usable
 from .dropout import check_dropout, on, same_rows
 from .functional import _TORCH_DTYPE, check_tensor
 
@@ -209,7 +209,7 @@ class ResidualJoin(_Rows):
 class _NormFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, norm, x, gamma, beta):
-        x = x.contiguous()
+        x = usable(x)
         ctx.norm = norm
         ctx.save_for_backward(x, gamma, beta)
         return norm.forward(x, gamma, beta)
@@ -219,7 +219,7 @@ class _NormFn(torch.autograd.Function):
     def backward(ctx, dh):
         x, gamma, beta = ctx.saved_tensors
         want = any(ctx.needs_input_grad[2:])
-        dx, dgamma, dbeta = ctx.norm.backward(x, dh.contiguous(), gamma, beta, want_params=want)
+        dx, dgamma, dbeta = ctx.norm.backward(x, usable(dh), gamma, beta, want_params=want)
         return None, dx, dgamma, dbeta
 
 
@@ -231,7 +231,7 @@ def block_norm(norm, x, gamma=None, beta=None):
 class _JoinFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, join, x, z, post_gamma, post_beta, scale, gate, pre_gamma, pre_beta, drop, path):
-        x, z = x.contiguous(), z.contiguous()
+        x, z = usable(x), usable(z)
         params = (post_gamma, post_beta, scale, gate, pre_gamma, pre_beta)
         y, h = join.forward(x, z, *params, drop=drop, path=path)
         ctx.join, ctx.drop, ctx.path = join, drop, path
@@ -247,7 +247,7 @@ class _JoinFn(torch.autograd.Function):
         y, z, *params = ctx.saved_tensors[:8]
         if dy is None and dh is None:
             return (None,) * 11
-        dy, dh = (None if g is None else g.contiguous() for g in (dy, dh))
+        dy, dh = (None if g is None else usable(g) for g in (dy, dh))
         g = ctx.join.backward(y, z, dy, dh, *params, drop=ctx.drop, path=ctx.path,
                               want_params=any(ctx.needs_input_grad[3:9]))
         return (None, *g, None, None)

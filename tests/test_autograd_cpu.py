@@ -102,3 +102,47 @@ def test_first_derivatives_stay(name, slope):
         x = torch.full((4,), 2.0, requires_grad=True)
         g, = torch.autograd.grad(CALLS[name](x).sum(), x, create_graph=graph)
         assert g.tolist() == [slope] * 4
+
+
+class Seen:
+    """A stand-in's passes with the tensors that reach them."""
+
+    def __init__(self, inner):
+        self.inner, self.tensors = inner, []
+        self.post, self.pre = getattr(inner, "post", None), getattr(inner, "pre", None)
+
+    def _see(self, args):
+        self.tensors += [a for a in args if isinstance(a, torch.Tensor) and a.dim()]
+
+    def forward(self, *args, **kwargs):
+        self._see(args)
+        return self.inner.forward(*args, **kwargs)
+
+    def backward(self, *args, **kwargs):
+        self._see(args)
+        return self.inner.backward(*args, **kwargs)
+
+
+@pytest.mark.parametrize("name", ["attention", "norm", "join", "dropout"])
+def test_tensors_off_a_16_byte_boundary_are_copied(name, monkeypatch):
+    """A slice of a larger tensor, and a gradient that arrives as one (of a concatenation), may start anywhere; the
+    library asks for 16 bytes, and the caller has no hand in where a gradient starts."""
+    seen = Seen({"attention": Attention(), "norm": Norm(), "join": Join()}.get(name))
+
+    def drop(x, drop, span=1):
+        seen.tensors.append(x)
+        return x * 2
+
+    monkeypatch.setattr(D, "apply_dropout", drop)
+    f = {"attention": lambda x: F.swin_window_attention(seen, x, x, x), "norm": lambda x: R.block_norm(seen, x),
+         "join": lambda x: R.residual_join(seen, x, x)[0], "dropout": lambda x: D.dropout(x, None)}[name]
+    grads = []
+    for shift in (0, 1):  # elements of 4 bytes
+        leaf = torch.cat([torch.zeros(shift), torch.arange(1.0, 5.0)]).requires_grad_(True)
+        x = leaf[shift:]
+        assert x.is_contiguous() and x.data_ptr() % 16 == 4 * shift
+        y = torch.cat([torch.zeros(shift), f(x)])
+        (y * torch.cat([torch.zeros(shift), torch.arange(5.0, 9.0)])).sum().backward()
+        grads.append(leaf.grad[shift:])
+    assert torch.equal(*grads)
+    assert seen.tensors and all(t.is_contiguous() and t.data_ptr() % 16 == 0 for t in seen.tensors)

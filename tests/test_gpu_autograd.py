@@ -33,3 +33,18 @@ def test_second_derivatives_are_refused(name):
             continue
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (y.sum() + g.square().sum()).backward()
+
+
+@pytest.mark.parametrize("name", ["attention", "attention_dropout", "norm", "join", "dropout"])
+def test_tensors_that_start_anywhere(name):
+    """A slice as the input and a concatenation's slice as the gradient give what aligned tensors give."""
+    f = calls()[name]
+    x = torch.randn(1, 9, 13, 64, device="cuda")
+    w = torch.randn(x.numel(), device="cuda")
+    got = []
+    for shift in (0, 1):
+        leaf = torch.cat([x.new_zeros(shift), x.flatten()]).requires_grad_(True)
+        y = torch.cat([x.new_zeros(shift), f(leaf[shift:].view(x.shape)).flatten()])
+        (y[shift:] * w).sum().backward()
+        got.append((y[shift:].detach(), leaf.grad[shift:]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
