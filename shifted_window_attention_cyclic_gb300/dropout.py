@@ -44,7 +44,8 @@ class Dropout:
 
     The rate takes effect as T / 65536, T = round(rate * 65536); what is kept
     is scaled by 1 / (1 - T / 65536). Dropouts of one step need different
-    sites, or they drop the same positions.
+    sites, or they drop the same positions. None of the three changes later:
+    for another rate (none, in an evaluation) pass another Dropout (or None).
     """
 
     def __init__(self, state, rate, site):
@@ -54,12 +55,16 @@ class Dropout:
             raise ValueError("rate: from 0 to 65535/65536, got %r" % (rate,))
         if int(site) != site or not 0 <= site < 2 ** 32:
             raise ValueError("site: a whole number of 32 bits, got %r" % (site,))
-        self.state, self.rate, self.site = state, float(rate), int(site)
-        self.desc = C.swin_attn_drop(self.rate, self.site, state.tensor.data_ptr())
+        self._state, self._rate, self._site = state, float(rate), int(site)
+        self.desc = C.swin_attn_drop(self._rate, self._site, state.tensor.data_ptr())
+
+    state = property(lambda self: self._state)
+    rate = property(lambda self: self._rate)
+    site = property(lambda self: self._site)
 
     @property
     def active(self):
-        return round(self.rate * 65536) > 0
+        return round(self._rate * 65536) > 0
 
 
 def check_dropout(name, drop, device):
