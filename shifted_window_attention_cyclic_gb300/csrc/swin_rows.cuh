@@ -875,10 +875,14 @@ int launch_one(const RowArgs &a, int ctas, cudaStream_t st) {
   return cudaPeekAtLastError() == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
 }
 
-template <typename T, int TPR, int NV>
+// kBoth: a width that the backward with both norms takes too (width_of).
+template <typename T, int TPR, int NV, bool kBoth = true>
 int launch_rows(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cudaStream_t st) {
   if (bwd) {
-    if (branch && pre) return launch_one<T, TPR, NV, true, true, true>(a, ctas, st);
+    if (branch && pre) {
+      if constexpr (kBoth) return launch_one<T, TPR, NV, true, true, true>(a, ctas, st);
+      else return SWIN_ERR_UNSUPPORTED;  // not picked
+    }
     if (branch) return launch_one<T, TPR, NV, true, true, false>(a, ctas, st);
     return launch_one<T, TPR, NV, true, false, true>(a, ctas, st);
   }
@@ -893,13 +897,13 @@ int launch_width(const RowArgs &a, bool bwd, bool branch, bool pre, int ctas, cu
   if (wd.tpr == 2) return launch_rows<T, 2, 1>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 4 && wd.nv == 1) return launch_rows<T, 4, 1>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 4 && wd.nv == 2) return launch_rows<T, 4, 2>(a, bwd, branch, pre, ctas, st);
-  if (wd.tpr == 4) return launch_rows<T, 4, 3>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 4) return launch_rows<T, 4, 3, false>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 8 && wd.nv == 2) return launch_rows<T, 8, 2>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 8) return launch_rows<T, 8, 3>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 16 && wd.nv == 2) return launch_rows<T, 16, 2>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 16) return launch_rows<T, 16, 3>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 32 && wd.nv == 2) return launch_rows<T, 32, 2>(a, bwd, branch, pre, ctas, st);
-  if (wd.tpr == 32) return launch_rows<T, 32, 3>(a, bwd, branch, pre, ctas, st);
+  if (wd.tpr == 32) return launch_rows<T, 32, 3, false>(a, bwd, branch, pre, ctas, st);
   if (wd.tpr == 128) return launch_rows<T, 128, 1>(a, bwd, branch, pre, ctas, st);
   if constexpr (sizeof(T) == 2)
     if (wd.tpr == 160) return launch_rows<T, 160, 2>(a, bwd, branch, pre, ctas, st);
