@@ -326,7 +326,8 @@ int swin_attn_norm_bwd(const swin_attn_rows *rows, const void *x, const swin_att
 typedef struct {
   swin_attn_norm post, pre;
   const float *scale; /* [C] layer scale; NULL: ones */
-  const float *gate;  /* [images][C]; NULL: ones */
+  const float *gate;  /* [images][C]; NULL: ones. Post-side parameter gradients beside a gate: up to
+                         16 776 960 images (else UNSUPPORTED) */
   swin_attn_drop drop, path;
 } swin_attn_join;
 
@@ -352,6 +353,7 @@ int swin_attn_join_bwd(const swin_attn_rows *rows, const void *y, const void *z,
 /* Dropout of n elements of type dtype: y_i = keep(i / span) ? x_i / kept : 0,
  * `span` consecutive elements sharing one decision (1: dropout; tokens * C:
  * stochastic depth per image). Its backward is the same call on the gradient.
+ * n < 0 or above 2^46, or span < 1, is INVALID_ARG.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA. */
 int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, const swin_attn_drop *drop, void *y,
                       swin_stream_t stream);
