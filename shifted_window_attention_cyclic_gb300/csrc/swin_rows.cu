@@ -265,7 +265,7 @@ struct Range {
 };
 bool meet(const Range &a, const Range &b) {
   const uintptr_t p = reinterpret_cast<uintptr_t>(a.at), q = reinterpret_cast<uintptr_t>(b.at);
-  return p && q && p < q + b.bytes && q < p + a.bytes;
+  return p && q && a.bytes && b.bytes && p < q + b.bytes && q < p + a.bytes;
 }
 template <int kOut, int kIn>
 bool clash(const Range (&out)[kOut], const Range (&in)[kIn]) {

@@ -50,3 +50,11 @@ def test_parameter_gradients_over_anything_but_their_parameter(lib):
     drop = C.swin_attn_drop(0.1, 0, P + 0x9000)
     j = join(drop=drop, scale=P)
     assert jb(scale=P + 0x9000) == bad
+
+
+def test_nothing_overlaps_an_empty_tensor(lib):
+    """Without rows the activations are empty, wherever their pointers point. (Refused later, for want of a workspace.)"""
+    r, P = rows(images=2, tokens=0, channels=32, dtype=C.SWIN_F32), 0xA0000000
+    assert lib.swin_attn_norm_bwd(r, P + 16, norm(), P + 32, None, P + 64, P, None, None, 0, None) != C.SWIN_ERR_INVALID_ARG
+    g = C.swin_attn_join_grads(scale=P)
+    assert lib.swin_attn_join_bwd(r, P + 16, B2, join(), C3, D4, P + 32, P + 64, g, None, 0, None) != C.SWIN_ERR_INVALID_ARG
