@@ -441,6 +441,11 @@ int run_backward(RowArgs &a, const swin_attn_rows *r, bool branch, const swin_at
     a.part_pre = want_pre ? ws : nullptr;
     a.part_post = want_post ? ws + (size_t)sp.ctas * 2 * a.C : nullptr;
   }
+  if (!pre) {  // of a join whose h no gradient reached
+    const size_t cb = sizeof(float) * a.C;
+    if (g.pre_gamma && cudaMemsetAsync(g.pre_gamma, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
+    if (g.pre_beta && cudaMemsetAsync(g.pre_beta, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
+  }
   if (a.rows) {
     rc = r->dtype == SWIN_BF16 ? launch_bf16(a, true, branch, pre, sp.ctas, st)
                                : launch_f32(a, true, branch, pre, sp.ctas, st);
@@ -589,12 +594,7 @@ int swin_attn_join_bwd(const swin_attn_rows *r, const void *y, const void *z, co
   a.wide = !mis(dx, 32) && !mis(dz, 32);
   a.scale = join->scale;
   a.gate = join->gate;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (pre && !dh) {
-    if (grads->pre_gamma && cudaMemsetAsync(grads->pre_gamma, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
-    if (grads->pre_beta && cudaMemsetAsync(grads->pre_beta, 0, cb, st) != cudaSuccess) return SWIN_ERR_CUDA;
-  }
-  return run_backward(a, r, true, *grads, workspace, workspace_bytes, st);
+  return run_backward(a, r, true, *grads, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, const swin_attn_drop *drop, void *y,

@@ -47,3 +47,21 @@ def test_norm_gradients_over_their_parameters():
     dx = torch.empty_like(x)
     C.swin_attn_norm_bwd(rows, x, norm, dh, None, dx, gamma, beta, ws)
     assert torch.equal(dx, want[0]) and torch.equal(gamma, want[1]) and torch.equal(beta, want[2])
+
+
+def test_a_refused_call_writes_nothing():
+    """Without a gradient of h the pre norm's gradients are zeroed, but not by a call that is refused."""
+    from shifted_window_attention_cyclic_gb300 import swin_attn as C
+    x = torch.randn(2, 50, 64, device="cuda")
+    grads = {n: torch.full((64,), 7.0, device="cuda") for n in ("pre_gamma", "pre_beta", "scale")}
+    norm, none, off = C.swin_attn_norm(C.SWIN_NORM_LAYER, 1e-5, None, None), C.swin_attn_norm(0, 1e-5, None, None), C.swin_attn_drop(0.0, 0, None)
+    rows, join = C.swin_attn_rows(2, 50, 64, C.SWIN_F32), C.swin_attn_join(none, norm, None, None, off, off)
+    dx, dz = torch.empty_like(x), torch.empty_like(x)
+    desc = C.swin_attn_join_grads(**{n: t.data_ptr() for n, t in grads.items()})
+    with pytest.raises(C.SwinAttnError, match=r"\(%d\)" % C.SWIN_ERR_WORKSPACE):
+        C.swin_attn_join_bwd(rows, x, x, join, x, None, dx, dz, desc, None)
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in grads.values())
+    ws = torch.empty(C.swin_attn_rows_workspace_bytes(rows), dtype=torch.uint8, device="cuda")
+    C.swin_attn_join_bwd(rows, x, x, join, x, None, dx, dz, desc, ws)
+    assert not grads["pre_gamma"].any() and not grads["pre_beta"].any() and grads["scale"].ne(7).all()
