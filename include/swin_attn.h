@@ -358,6 +358,76 @@ int swin_attn_join_bwd(const swin_attn_rows *rows, const void *y, const void *z,
 int swin_attn_dropout(int32_t dtype, int64_t n, int64_t span, const void *x, const swin_attn_drop *drop, void *y,
                       swin_stream_t stream);
 
+/* ---- Between the projection and the attention: heads and their positions ----
+ * The QKV projection leaves rows [q | k | v]; the attention takes q, k and v as
+ * tensors of their own. These calls read up to four parts (of one packed tensor
+ * or of several), norm every head, turn its values by the token's position, and
+ * write each part where it is wanted, in one pass; and back. Per part, token and
+ * head, with u = N(x) (gamma and beta [head_dim], shared by the part's heads):
+ *   pair i of the first rotary.dim values of u, (a, b) = (u_i, u_{i + dim/2}) in the
+ *   half layout, (u_2i, u_{2i+1}) in the interleaved one, becomes
+ *   A (a cos t - b sin t), A (a sin t + b cos t) with t = position[axis_i] * f_i;
+ *   the other values are u's.
+ * Angles are kept in turns as 64-bit fixed point, freq_i = round(2^64 f_i / (2 pi))
+ * modulo 2^64: a position times it wraps by itself, so the error of an angle is
+ * |position| 2^-65 turns and no position is too far. Sums are fp32 in a fixed
+ * order; each value is rounded once, when it is stored.
+ * The rules of the rows' calls (above) hold: current device, nothing allocated,
+ * asynchronous, alignments (rows' strides too: multiples of 16 bytes). A part's
+ * output may lie exactly on its own x (forward), x or dy (backward), with the
+ * same stride; any other overlap of an output with another output, an input or
+ * the workspace is INVALID_ARG. Rows of one stride that lie side by side, as the
+ * parts of a packed tensor do, do not overlap. */
+#define SWIN_ROTARY_HALF 0
+#define SWIN_ROTARY_INTERLEAVED 1
+typedef struct {
+  int32_t dim;           /* values of a head that turn: a multiple of 16 up to head_dim; 0: none */
+  int32_t layout;        /* SWIN_ROTARY_* */
+  float amplitude;       /* A, finite */
+  const uint64_t *freq;  /* HOST [dim / 2], read by the call */
+  const uint8_t *axis;   /* HOST [dim / 2], each below ndim */
+  int32_t position_bits; /* 0: a token's grid coordinates are its positions; 32 or 64: they are given */
+  int32_t shared;        /* given positions are 0: [images][tokens][ndim], 1: [tokens][ndim] of every image */
+  const void *positions; /* device, int32 or int64 (aligned to them), any sign; NULL with grid coordinates */
+} swin_attn_rotary;
+
+typedef struct {
+  int64_t images;   /* >= 0; images * tokens < 2^31 (else UNSUPPORTED) */
+  int32_t ndim;     /* 1 to 3 */
+  int32_t grid[3];  /* tokens of an image, outermost first, >= 0 */
+  int32_t head_dim; /* a multiple of 16 up to 256 (else UNSUPPORTED) */
+  int32_t dtype;    /* SWIN_F32 or SWIN_BF16 */
+  swin_attn_rotary rotary;
+} swin_attn_heads;
+
+#define SWIN_HEAD_PARTS_MAX 4
+typedef struct {
+  int32_t heads;        /* 1 to 65535 */
+  int32_t rotate;       /* 0 or 1; neither this nor a norm: the part is copied */
+  swin_attn_norm norm;  /* gamma, beta: [head_dim] */
+  const void *x;        /* [images * tokens] rows of heads * head_dim values */
+  int64_t x_stride;     /* elements from row to row, at least heads * head_dim */
+  const void *dy;       /* backward: the gradient of the part's output (forward: ignored) */
+  int64_t dy_stride;
+  void *out;            /* forward: the part's output; backward: dx */
+  int64_t out_stride;
+  float *dgamma, *dbeta; /* backward: overwritten; NULL: not wanted. Not without a norm */
+} swin_attn_head_part;
+
+/* Forward of `count` parts. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA. */
+int swin_attn_heads_fwd(const swin_attn_heads *heads, const swin_attn_head_part *parts, int32_t count,
+                        swin_stream_t stream);
+
+/* Bytes of device workspace that swin_attn_heads_bwd needs for dgamma and dbeta (0 for a bad descriptor). */
+size_t swin_attn_heads_workspace_bytes(const swin_attn_heads *heads);
+
+/* Backward: dx of every part, x being its forward's input (NULL for a part
+ * without a norm: it is not read). The statistics are recomputed. The workspace
+ * is needed for dgamma or dbeta only (WORKSPACE).
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+int swin_attn_heads_bwd(const swin_attn_heads *heads, const swin_attn_head_part *parts, int32_t count,
+                        void *workspace, size_t workspace_bytes, swin_stream_t stream);
+
 /* Testing hook for the failure path of the tensor-core kernels (the fused
  * block's included). Every wait inside those kernels gives up after
  * `wait_limit_ns` (default 1 s) and then records SWIN_ERR_TIMEOUT in the

@@ -23,9 +23,9 @@
 // registers and the column sums (the parameter gradients) accumulate there,
 // per CTA, and are folded in a fixed order by a second kernel: no atomics, the
 // same bits every run. All sums and statistics are fp32.
-#include <atomic>
 #include <cmath>
 
+#include "swin_calls.cuh"
 #include "swin_rows.cuh"
 
 namespace swin {
@@ -218,21 +218,7 @@ __global__ void __launch_bounds__(256) dropout_kernel(const T *x, T *y, int64_t 
   }
 }
 
-// ---- launches ----------------------------------------------------------------------
-// SMs of the current device (asked once per device: the calls are short).
-int sm_count(int *sms) {
-  static std::atomic<int> known[64];
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return SWIN_ERR_CUDA;
-  if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return SWIN_OK;
-  if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SWIN_ERR_CUDA;
-  if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
-  return SWIN_OK;
-}
-
 // ---- argument checks ---------------------------------------------------------------
-bool mis(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
 int check_rows(const swin_attn_rows *r, int64_t *rows, size_t *bytes) {
   if (!r || r->images < 0 || r->tokens < 0) return SWIN_ERR_INVALID_ARG;
   if (r->dtype != SWIN_F32 && r->dtype != SWIN_BF16) return SWIN_ERR_UNSUPPORTED;
@@ -407,16 +393,7 @@ namespace {
 // As a programmatic dependent of the kernel before it in the stream: its launch
 // overlaps that kernel's end (the fold took 10 us behind a backward of 80 us).
 int launch_columns(const ColArgs &c, int tiles, unsigned groups, cudaStream_t st) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles, groups, 2);
-  cfg.blockDim = dim3(32, kColLanes);
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, columns_kernel, c) == cudaSuccess ? SWIN_OK : SWIN_ERR_CUDA;
+  return launch_dependent(columns_kernel, dim3(tiles, groups, 2), dim3(32, kColLanes), 0, st, c);
 }
 
 // Row pass and parameter gradients of the two backward entry points.

@@ -40,6 +40,8 @@ SWIN_IMPL_TC = 2
 SWIN_NORM_NONE = 0
 SWIN_NORM_LAYER = 1
 SWIN_NORM_RMS = 2
+SWIN_ROTARY_HALF = 0
+SWIN_ROTARY_INTERLEAVED = 1
 
 
 class SwinAttnError(RuntimeError):
@@ -87,6 +89,24 @@ class swin_attn_join_grads(ctypes.Structure):
                                                      "pre_beta")]
 
 
+class swin_attn_rotary(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("freq", ctypes.c_void_p), ("axis", ctypes.c_void_p), ("position_bits", ctypes.c_int32),
+                ("shared", ctypes.c_int32), ("positions", ctypes.c_void_p)]
+
+
+class swin_attn_heads(ctypes.Structure):
+    _fields_ = [("images", ctypes.c_int64), ("ndim", ctypes.c_int32), ("grid", ctypes.c_int32 * 3),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rotary", swin_attn_rotary)]
+
+
+class swin_attn_head_part(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("rotate", ctypes.c_int32), ("norm", swin_attn_norm),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("dy", ctypes.c_void_p),
+                ("dy_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("dgamma", ctypes.c_void_p), ("dbeta", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -132,6 +152,13 @@ def load_library():
     lib.swin_attn_join_bwd.restype = ctypes.c_int
     lib.swin_attn_dropout.argtypes = [i32, i64, i64, vp, ctypes.POINTER(swin_attn_drop), vp, vp]
     lib.swin_attn_dropout.restype = ctypes.c_int
+    heads, part = ctypes.POINTER(swin_attn_heads), ctypes.POINTER(swin_attn_head_part)
+    lib.swin_attn_heads_fwd.argtypes = [heads, part, i32, vp]
+    lib.swin_attn_heads_fwd.restype = ctypes.c_int
+    lib.swin_attn_heads_workspace_bytes.argtypes = [heads]
+    lib.swin_attn_heads_workspace_bytes.restype = sz
+    lib.swin_attn_heads_bwd.argtypes = [heads, part, i32, vp, sz, vp]
+    lib.swin_attn_heads_bwd.restype = ctypes.c_int
     lib.swin_attn_bwd_noalloc.argtypes = [vp] * 13
     lib.swin_attn_bwd_noalloc.restype = ctypes.c_int
     lib.swin_attn_block_fwd.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -359,6 +386,21 @@ def swin_attn_join_bwd(rows: swin_attn_rows, y, z, join: swin_attn_join, dy, dh,
 def swin_attn_dropout(dtype: int, n: int, span: int, x, drop: swin_attn_drop, y, stream=None) -> None:
     _check(load_library().swin_attn_dropout(dtype, n, span, _addr(x), drop, _addr(y), _handle(stream)),
            "swin_attn_dropout")
+
+
+def swin_attn_heads_workspace_bytes(heads: swin_attn_heads) -> int:
+    return load_library().swin_attn_heads_workspace_bytes(heads)
+
+
+def swin_attn_heads_fwd(heads: swin_attn_heads, parts, count: int, stream=None) -> None:
+    """`parts`: a ctypes array of swin_attn_head_part."""
+    _check(load_library().swin_attn_heads_fwd(heads, parts, count, _handle(stream)), "swin_attn_heads_fwd")
+
+
+def swin_attn_heads_bwd(heads: swin_attn_heads, parts, count: int, workspace, stream=None) -> None:
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load_library().swin_attn_heads_bwd(heads, parts, count, _addr(workspace), ws_bytes, _handle(stream)),
+           "swin_attn_heads_bwd")
 
 
 def swin_attn_bwd_noalloc(plan: Plan, q, k, v, dout, lse, bias, land, dq, dk, dv, dbias, stream=None) -> None:
