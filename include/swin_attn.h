@@ -428,6 +428,59 @@ size_t swin_attn_heads_workspace_bytes(const swin_attn_heads *heads);
 int swin_attn_heads_bwd(const swin_attn_heads *heads, const swin_attn_head_part *parts, int32_t count,
                         void *workspace, size_t workspace_bytes, swin_stream_t stream);
 
+/* ---- After the backward: the parameters' step --------------------------------
+ * One AdamW step over many tensors, and the global norm of their gradients. The
+ * step count and the learning rate lie on the device and are read when the
+ * kernels run, so a captured step replays with what it finds there.
+ *   c = min(1, max_norm / |g|), |g| over all tensors of the call (c = 1 without max_norm),
+ *   g' = c g, m = b1 m + (1 - b1) g', v = b2 v + (1 - b2) g'^2, t = steps so far + 1,
+ *   w = w (1 - lr decay) - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps).
+ * A bf16 parameter is the rounded copy of an fp32 master weight. States are fp32,
+ * or 8 bits: m and r = sqrt(v) in e4m3 times one fp32 scale of every 256
+ * consecutive values of a tensor (the largest magnitude over 448), rounded to
+ * nearest when stored (the step itself uses the unrounded ones); an r above 0 is
+ * stored as 2^-9 of a scale at least, so that no denominator vanishes.
+ * With max_norm, a gradient norm that is not finite (squares are fp32: magnitudes
+ * above 1.8e19 count as infinite) leaves parameters, states and step count as
+ * they are. Everything is fp32, sums in a fixed order: the same bits every run. */
+typedef struct {
+  int64_t n;         /* elements, >= 0 (0: skipped) */
+  int32_t dtype;     /* of param: SWIN_F32 or SWIN_BF16 */
+  int32_t grad_dtype;
+  void *param;       /* updated */
+  float *master;     /* SWIN_BF16: updated; NULL otherwise */
+  const void *grad;  /* NULL: the tensor is skipped */
+  void *m, *v;       /* [n] float, or bytes of e4m3 (v holds r) */
+  float *m_scale, *v_scale; /* 8 bits: [ceil(n / 256)]; NULL otherwise */
+  float decay;       /* weight decay, finite, >= 0 */
+} swin_attn_param;
+
+typedef struct {
+  double beta1, beta2;  /* 0 <= beta < 1 */
+  double eps;           /* > 0, finite */
+  double max_norm;      /* > 0: clip; 0: do not */
+  int32_t state_bits;   /* 32 or 8 */
+  const float *lr;      /* device */
+  int64_t *steps;       /* device: steps so far, counted up by the call */
+  float *norm;          /* device, NULL: not wanted (with max_norm only): |g| before clipping */
+} swin_attn_adamw;
+
+/* Bytes of device workspace that the two calls below need. */
+size_t swin_attn_adamw_workspace_bytes(void);
+
+/* One step. Elements are aligned to their own size, the workspace to 256 bytes;
+ * outputs (param, master, m, v, scales, steps, norm, workspace) overlap neither
+ * one another nor any input (INVALID_ARG). All tensors' elements together, each
+ * tensor's rounded up to 256: below 2^39 (else UNSUPPORTED).
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+int swin_attn_adamw_step(const swin_attn_adamw *adamw, const swin_attn_param *params, int64_t count,
+                         void *workspace, size_t workspace_bytes, swin_stream_t stream);
+
+/* norm = sqrt(sum of squares) of the gradients in params (n, grad, grad_dtype; the rest is ignored).
+ * Errors: INVALID_ARG, ALIGNMENT, WORKSPACE, UNSUPPORTED, CUDA. */
+int swin_attn_grad_norm(const swin_attn_param *params, int64_t count, float *norm, void *workspace,
+                        size_t workspace_bytes, swin_stream_t stream);
+
 /* Testing hook for the failure path of the tensor-core kernels (the fused
  * block's included). Every wait inside those kernels gives up after
  * `wait_limit_ns` (default 1 s) and then records SWIN_ERR_TIMEOUT in the

@@ -107,6 +107,19 @@ class swin_attn_head_part(ctypes.Structure):
                 ("dgamma", ctypes.c_void_p), ("dbeta", ctypes.c_void_p)]
 
 
+class swin_attn_param(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("param", ctypes.c_void_p), ("master", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("decay", ctypes.c_float)]
+
+
+class swin_attn_adamw(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("max_norm", ctypes.c_double), ("state_bits", ctypes.c_int32), ("lr", ctypes.c_void_p),
+                ("steps", ctypes.c_void_p), ("norm", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -152,13 +165,19 @@ def load_library():
     lib.swin_attn_join_bwd.restype = ctypes.c_int
     lib.swin_attn_dropout.argtypes = [i32, i64, i64, vp, ctypes.POINTER(swin_attn_drop), vp, vp]
     lib.swin_attn_dropout.restype = ctypes.c_int
-    heads, part = ctypes.POINTER(swin_attn_heads), ctypes.POINTER(swin_attn_head_part)
+    heads, part, param = (ctypes.POINTER(t) for t in (swin_attn_heads, swin_attn_head_part, swin_attn_param))
     lib.swin_attn_heads_fwd.argtypes = [heads, part, i32, vp]
     lib.swin_attn_heads_fwd.restype = ctypes.c_int
     lib.swin_attn_heads_workspace_bytes.argtypes = [heads]
     lib.swin_attn_heads_workspace_bytes.restype = sz
     lib.swin_attn_heads_bwd.argtypes = [heads, part, i32, vp, sz, vp]
     lib.swin_attn_heads_bwd.restype = ctypes.c_int
+    lib.swin_attn_adamw_workspace_bytes.argtypes = []
+    lib.swin_attn_adamw_workspace_bytes.restype = sz
+    lib.swin_attn_adamw_step.argtypes = [ctypes.POINTER(swin_attn_adamw), param, i64, vp, sz, vp]
+    lib.swin_attn_adamw_step.restype = ctypes.c_int
+    lib.swin_attn_grad_norm.argtypes = [param, i64, vp, vp, sz, vp]
+    lib.swin_attn_grad_norm.restype = ctypes.c_int
     lib.swin_attn_bwd_noalloc.argtypes = [vp] * 13
     lib.swin_attn_bwd_noalloc.restype = ctypes.c_int
     lib.swin_attn_block_fwd.argtypes = [vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
@@ -401,6 +420,21 @@ def swin_attn_heads_bwd(heads: swin_attn_heads, parts, count: int, workspace, st
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(load_library().swin_attn_heads_bwd(heads, parts, count, _addr(workspace), ws_bytes, _handle(stream)),
            "swin_attn_heads_bwd")
+
+
+def swin_attn_adamw_workspace_bytes() -> int:
+    return load_library().swin_attn_adamw_workspace_bytes()
+
+
+def swin_attn_adamw_step(adamw: swin_attn_adamw, params, count: int, workspace, stream=None) -> None:
+    """`params`: a ctypes array of swin_attn_param."""
+    _check(load_library().swin_attn_adamw_step(adamw, params, count, _addr(workspace), workspace.numel(),
+                                               _handle(stream)), "swin_attn_adamw_step")
+
+
+def swin_attn_grad_norm(params, count: int, norm, workspace, stream=None) -> None:
+    _check(load_library().swin_attn_grad_norm(params, count, _addr(norm), _addr(workspace), workspace.numel(),
+                                              _handle(stream)), "swin_attn_grad_norm")
 
 
 def swin_attn_bwd_noalloc(plan: Plan, q, k, v, dout, lse, bias, land, dq, dk, dv, dbias, stream=None) -> None:
