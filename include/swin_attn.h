@@ -402,7 +402,7 @@ typedef struct {
 
 #define SWIN_HEAD_PARTS_MAX 4
 typedef struct {
-  int32_t heads;        /* 1 to 65535 */
+  int32_t heads;        /* 1 to 65535, heads * head_dim up to 16384 (else UNSUPPORTED) */
   int32_t rotate;       /* 0 or 1; neither this nor a norm: the part is copied */
   swin_attn_norm norm;  /* gamma, beta: [head_dim] */
   const void *x;        /* [images * tokens] rows of heads * head_dim values */

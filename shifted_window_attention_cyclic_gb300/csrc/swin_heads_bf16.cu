@@ -4,8 +4,8 @@
 namespace swin {
 namespace heads {
 
-int launch_bf16(const Args &a, bool bwd, bool norm, int ctas, size_t smem, cudaStream_t st) {
-  return launch_heads<__nv_bfloat16>(a, bwd, norm, ctas, smem, st);
+int launch_bf16(const Args &a, bool bwd, bool norm, bool beta, int ctas, size_t smem, cudaStream_t st) {
+  return launch_heads<__nv_bfloat16>(a, bwd, norm, beta, ctas, smem, st);
 }
 
 }  // namespace heads

@@ -4,8 +4,8 @@
 namespace swin {
 namespace heads {
 
-int launch_f32(const Args &a, bool bwd, bool norm, int ctas, size_t smem, cudaStream_t st) {
-  return launch_heads<float>(a, bwd, norm, ctas, smem, st);
+int launch_f32(const Args &a, bool bwd, bool norm, bool beta, int ctas, size_t smem, cudaStream_t st) {
+  return launch_heads<float>(a, bwd, norm, beta, ctas, smem, st);
 }
 
 }  // namespace heads

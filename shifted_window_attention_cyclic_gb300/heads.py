@@ -146,8 +146,8 @@ class AttentionHeads:
         if int(head_dim) != head_dim or head_dim < 16 or head_dim % 16 or head_dim > 256:
             raise ValueError("head_dim: a multiple of 16 from 16 to 256, got %r" % (head_dim,))
         for name, n in (("heads", heads), ("kv_heads", heads if kv_heads is None else kv_heads)):
-            if int(n) != n or not 1 <= n <= 65535:
-                raise ValueError("%s: 1 to 65535, got %r" % (name, n))
+            if int(n) != n or n < 1 or n * head_dim > 16384:
+                raise ValueError("%s: at least 1, and %s * head_dim up to 16384, got %r" % (name, name, n))
         if rotary is not None and not isinstance(rotary, Rotary):
             raise ValueError("rotary: expected a Rotary, got %s" % type(rotary).__name__)
         if rotary is not None and rotary.dim > head_dim:

@@ -114,6 +114,16 @@ def test_many_tiles():
         check(gen, spec, 2, (61, 1023), packed=heads != 3)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_many_heads(dtype):
+    """More heads than a CTA takes at a time: a row in chunks, the last one ragged."""
+    from shifted_window_attention_cyclic_gb300.heads import AttentionHeads, Rotary
+    gen = torch.Generator().manual_seed(14)
+    for heads, kv, hd in ((64, 25, 256), (1024, 1, 16), (100, 13, 160)):
+        spec = AttentionHeads(heads, hd, Rotary(16, 1), "rms", 1e-5, dtype, kv)
+        check(gen, spec, 1, (19,))
+
+
 def test_large_mean():
     """Heads far from zero: the mean is taken out before the squares."""
     from shifted_window_attention_cyclic_gb300.heads import AttentionHeads

@@ -67,7 +67,7 @@ def test_bad_descriptors(lib):
 
 def test_bad_parts(lib):
     d = heads()
-    for p, code in ((part(n=0), BAD), (part(n=65536), BAD), (part(rotate=2), BAD), (part(x=None), BAD), (part(out=None), BAD),
+    for p, code in ((part(n=0), BAD), (part(n=65536), BAD), (part(n=513), UNSUP), (part(rotate=2), BAD), (part(x=None), BAD), (part(out=None), BAD),
                     (part(nm=norm(3)), BAD), (part(nm=norm(eps=0.0)), BAD), (part(nm=norm(eps=float("inf"))), BAD),
                     (part(nm=norm(0, gamma=C3)), BAD), (part(nm=norm(0, beta=C3)), BAD), (part(nm=norm(gamma=C3 + 2)), ALIGN),
                     (part(xs=63), BAD), (part(os=32), BAD), (part(xs=0), BAD), (part(xs=-64), BAD), (part(xs=2**61), BAD),
@@ -121,7 +121,7 @@ def test_bad_rotaries():
     for kw in (dict(heads=0, head_dim=32), dict(heads=2, head_dim=24), dict(heads=2, head_dim=272),
                dict(heads=2, head_dim=16, rotary=H.Rotary(32)), dict(heads=2, head_dim=32, rotary=16),
                dict(heads=2, head_dim=32, norm="batch"), dict(heads=2, head_dim=32, dtype="f16"),
-               dict(heads=2, head_dim=32, eps=0.0), dict(heads=2, head_dim=32, kv_heads=0)):
+               dict(heads=2, head_dim=32, eps=0.0), dict(heads=2, head_dim=32, kv_heads=0), dict(heads=65, head_dim=256)):
         with pytest.raises(ValueError):
             H.AttentionHeads(**kw)
 
