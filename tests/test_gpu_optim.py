@@ -177,12 +177,12 @@ def test_zero_gradients():
 def test_a_norm_that_is_not_finite_changes_nothing(value, bits):
     opt, grads, decays = group(4, [300, 70000, 5], KINDS["mixed"], bits, 1.0)
     opt.step(grads())
-    before = [p.clone() for p in opt.params] + [getattr(opt, n).clone().view(torch.uint8) for n in opt._STATE
+    before = [p.clone() for p in opt.params] + [getattr(opt, n).clone().reshape(-1).view(torch.uint8) for n in opt._STATE
                                                 if getattr(opt, n) is not None]
     bad = grads()
     bad[1][69999] = value
     opt.step(bad)
-    after = list(opt.params) + [getattr(opt, n).view(torch.uint8) for n in opt._STATE if getattr(opt, n) is not None]
+    after = list(opt.params) + [getattr(opt, n).reshape(-1).view(torch.uint8) for n in opt._STATE if getattr(opt, n) is not None]
     assert all(torch.equal(a, b) for a, b in zip(after, before)) and not torch.isfinite(opt.grad_norm).all()
     check_step(opt, grads(), decays, 1.0)  # and the next one counts on
 
