@@ -442,7 +442,8 @@ int swin_attn_heads_bwd(const swin_attn_heads *heads, const swin_attn_head_part 
  * stored as 2^-9 of a scale at least, so that no denominator vanishes.
  * With max_norm, a gradient norm that is not finite (squares are fp32: magnitudes
  * above 1.8e19 count as infinite) leaves parameters, states and step count as
- * they are. Everything is fp32, sums in a fixed order: the same bits every run. */
+ * they are; without it, an element whose gradient is not finite becomes NaN, in 8
+ * bits its 256 with it. Everything is fp32, sums in a fixed order: the same bits every run. */
 typedef struct {
   int64_t n;         /* elements, >= 0 (0: skipped) */
   int32_t dtype;     /* of param: SWIN_F32 or SWIN_BF16 */

@@ -113,10 +113,10 @@ int check_heads(const swin_attn_heads *h, int64_t *rows, int64_t *tokens) {
   return SWIN_OK;
 }
 
-// Values of a part's row: at most 6 chunks of a CTA's items (12 heads of 256 ... 192 of 16), which the
-// workspace counts on.
+// Values of a part's row: at most 10 chunks of a CTA's items (113 heads of 144, 12 at a time), which
+// the workspace counts on.
 constexpr int64_t kMostWidth = 16384;
-constexpr int kMostChunks = 6;
+constexpr int kMostChunks = 10;
 
 int run(const swin_attn_heads *h, const swin_attn_head_part *parts, int count, bool bwd, void *workspace,
         size_t workspace_bytes, cudaStream_t st) {

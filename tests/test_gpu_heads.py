@@ -10,6 +10,8 @@ two steps more (sincospif, 2 ulp): under 2^-22 in all, and again a step for the
 amplitude, so TURN = 2^-21 of the size. Parameter gradients add up to LONG more
 roundings (the items of a thread, then the fold). bf16 outputs add half a step,
 2^-8 of the value."""
+import gc
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -17,6 +19,15 @@ torch = pytest.importorskip("torch")
 from tests import heads_ref as ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_memory_kept():
+    """Give the allocator's blocks back: a later test counts what its calls hold, and a cached block may be the larger one."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 OPS, TURN, LONG = 64 * 2.0**-24, 2.0**-21, 256 * 2.0**-24
 TDT = {"bf16": torch.bfloat16, "f32": torch.float32}

@@ -2,11 +2,22 @@
 packed projection, head norm with rotary positions, the window attention with
 dropped probabilities, the residual join, the backward of all of them and the
 parameters' update; eager, and captured and replayed."""
+import gc
+
 import pytest
 
 torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_memory_kept():
+    """Give the allocator's blocks back: a later test counts what its calls hold, and a cached block may be the larger one."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 GRID, HEADS, HD = (12, 20), 2, 32
 C = HEADS * HD
