@@ -223,7 +223,7 @@ struct StepArgs {
 };
 
 // Step of 317 M bf16 weights with fp32 gradients in 8 bits, clipped: 1133 us with the
-// norm's 186, so 5.9 TB/s (88 % of the measured copy rate): latency at 32 warps an SM.
+// norm's 186, so 6.0 TB/s (89 % of the measured copy rate): latency at 32 warps an SM.
 // (A form of the loop's body for whole units and each gradient type, so that no
 // conversion waits in a branch: 1292 us.)
 template <bool k8, int kCount>

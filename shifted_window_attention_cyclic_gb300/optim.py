@@ -108,6 +108,8 @@ class AdamW:
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, max_norm=None):
         self.params, decays = [], []
+        if isinstance(params, torch.Tensor):
+            raise ValueError("params: a tensor, expected several (its rows are no parameters)")
         for group in params:
             some, decay = ([group], weight_decay) if not isinstance(group, dict) else (
                 list(group["params"]), group.get("weight_decay", weight_decay))

@@ -92,9 +92,11 @@ def test_bad_norms(lib):
 def test_bad_calls():
     x = torch.zeros(4)
     for call in (lambda: O.grad_norm([]), lambda: O.grad_norm([x]), lambda: O.grad_norm([None]), lambda: O.AdamW([]),
-                 lambda: O.AdamW([x]), lambda: O.AdamW([None]), lambda: O.AdamW([x], lr=float("nan")),
+                 lambda: O.AdamW([x]), lambda: O.AdamW([None]), lambda: O.AdamW(x), lambda: O.AdamW([x], lr=float("nan")),
                  lambda: O.AdamW([x], betas=(0.9, 1.0)), lambda: O.AdamW([x], betas=(0.9,)), lambda: O.AdamW([x], eps=0.0),
                  lambda: O.AdamW([x], weight_decay=-0.1), lambda: O.AdamW([{"params": [x], "weight_decay": float("inf")}]),
                  lambda: O.AdamW([x], state_bits=16), lambda: O.AdamW([x], max_norm=0.0), lambda: O.AdamW([x.double()])):
         with pytest.raises(ValueError):
             call()
+    with pytest.raises(ValueError, match="rows"):
+        O.AdamW(x)
