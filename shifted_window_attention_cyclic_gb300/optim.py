@@ -147,14 +147,14 @@ class AdamW:
             masters += -(-p.numel() // UNIT) * UNIT if p.dtype == torch.bfloat16 else 0
         state = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
         with torch.cuda.device(dev), torch.no_grad():
-            self.lr = torch.full((), float(lr), dtype=torch.float32, device=dev)
-            self.steps = torch.zeros((), dtype=torch.int64, device=dev)
-            self.grad_norm = None if max_norm is None else torch.zeros((), dtype=torch.float32, device=dev)
-            self.m, self.v = (torch.zeros(at * state.itemsize, dtype=torch.uint8, device=dev).view(state) for _ in range(2))
-            self.m_scale = self.v_scale = None
+            self._lr = torch.full((), float(lr), dtype=torch.float32, device=dev)
+            self._steps = torch.zeros((), dtype=torch.int64, device=dev)
+            self._grad_norm = None if max_norm is None else torch.zeros((), dtype=torch.float32, device=dev)
+            self._m, self._v = (torch.zeros(at * state.itemsize, dtype=torch.uint8, device=dev).view(state) for _ in range(2))
+            self._m_scale = self._v_scale = None
             if state_bits == 8:
-                self.m_scale, self.v_scale = (torch.zeros(at // UNIT, dtype=torch.float32, device=dev) for _ in range(2))
-            self.master = torch.zeros(masters, dtype=torch.float32, device=dev) if masters else None
+                self._m_scale, self._v_scale = (torch.zeros(at // UNIT, dtype=torch.float32, device=dev) for _ in range(2))
+            self._master = torch.zeros(masters, dtype=torch.float32, device=dev) if masters else None
             self._ws = torch.empty(C.swin_attn_adamw_workspace_bytes(), dtype=torch.uint8, device=dev)
             self._master_at, masters = [], 0
             for p in self.params:
@@ -181,6 +181,10 @@ class AdamW:
         a["param"] = self._held_at
         self._desc = C.swin_attn_adamw(*self.betas, self.eps, max_norm or 0.0, state_bits, self.lr.data_ptr(),
                                        self.steps.data_ptr(), None if max_norm is None else self.grad_norm.data_ptr())
+
+    # their addresses are what the calls take: write into them, there is no other in their place
+    lr, steps, grad_norm, m, v, m_scale, v_scale, master = (
+        property(attrgetter("_" + n)) for n in ("lr", "steps", "grad_norm", "m", "v", "m_scale", "v_scale", "master"))
 
     def step(self, grads=None, stream=None):
         """One step with `grads` (one for each parameter, bfloat16 or float32, None: the parameter is left

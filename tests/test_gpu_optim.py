@@ -311,6 +311,9 @@ def test_refusals_on_the_device():
             AdamW(ps)
     with pytest.raises(Exception):
         opt.step([p])  # a gradient over its parameter
+    for name in ("lr", "steps", "m", "v"):  # another tensor in the place of one whose address the calls take
+        with pytest.raises(AttributeError):
+            setattr(opt, name, 0.1)
     with pytest.raises(ValueError):
         grad_norm([p], out=torch.zeros(2, device="cuda"))
     p.data = torch.zeros(32, device="cuda")
